@@ -151,6 +151,39 @@ PA_API pa_status pa_paged_attention(void* out, const void* query, pa_dtype q_dty
                              void* workspace, size_t workspace_bytes, pa_stream_t stream);
 
 /*
+ * Workspace bytes of pa_paged_attention_accumulate: pa_paged_attention_workspace_size(...) plus the scaled
+ * scores of the step, 4 * num_seqs * num_heads * round_up(max_context_len, 64) bytes, and softmax statistics
+ * of 8 bytes per (sequence, head, partition). Returns 0 if the arguments are invalid. Makes no CUDA call.
+ */
+PA_API size_t pa_paged_attention_accumulate_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                                           int head_size, int max_context_len, int partition_size);
+
+/*
+ * pa_paged_attention that also adds the step's attention weights to the cached tokens' scores, the
+ * statistic that pa_evict_tokens evicts by. out is pa_paged_attention's, bit for bit, and with p_h its
+ * softmax weights of query head h, for every kv head k and token t < context_lens[s]:
+ *     scores[s][k][t] += sum of p_h[t] over the num_heads / num_kv_heads query heads h of k.
+ *
+ *  scores         [num_seqs][num_kv_heads][score_stride] fp32, read and written; row s belongs to sequence s
+ *                 of this batch (a token's entry starts at zero when the token is appended). Entries at and
+ *                 past context_lens[s] are neither read nor written.
+ *  score_stride   entries between the rows, >= max_context_len.
+ *  workspace      >= pa_paged_attention_accumulate_workspace_size(...); otherwise as pa_paged_attention's,
+ *                 and both calls may share it in stream order.
+ * Everything else is as in pa_paged_attention. Weights are formed in fp32 from the unrounded scores. A block
+ * id outside the pool (PA_DEVERR_BLOCK_ID) makes its sequence's scores NaN up to its length in the kv heads
+ * that read it; an invalid length (PA_DEVERR_CONTEXT_LEN) leaves the sequence's scores as they are.
+ */
+PA_API pa_status pa_paged_attention_accumulate(void* out, float* scores, int score_stride, const void* query,
+                                               pa_dtype q_dtype, const void* key_cache, const void* value_cache,
+                                               pa_dtype kv_dtype, const float* k_scale, const float* v_scale,
+                                               const int32_t* block_tables, int max_blocks_per_seq,
+                                               const int32_t* context_lens, int num_seqs, int num_heads,
+                                               int num_kv_heads, int head_size, int block_size, int num_blocks,
+                                               int max_context_len, float scale, int partition_size,
+                                               void* workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
  * Paged attention without a caller-allocated workspace. The pages have no counterpart: this entry
  * point exists for callers that cannot call cudaMalloc -- a plugin hosted by an engine that owns all
  * device memory, or a serving loop that must not allocate (nor pay cudaMalloc's implicit device
@@ -224,6 +257,71 @@ PA_API pa_status pa_paged_prefill(void* out, const void* query, pa_dtype q_dtype
                                   size_t workspace_bytes, pa_stream_t stream);
 
 /*
+ * Workspace bytes of pa_paged_prefill_accumulate: the header and one fp32 statistic per query row and head,
+ * PA_WORKSPACE_HEADER_BYTES + round_up(4 * num_q_tokens * num_heads, 256). 0 if the arguments are invalid.
+ */
+PA_API size_t pa_paged_prefill_accumulate_workspace_size(int num_q_tokens, int num_heads);
+
+/*
+ * pa_paged_prefill that also adds the chunk's attention weights to the cached tokens' scores. out is
+ * pa_paged_prefill's, bit for bit, and with p_jh its softmax weights of chunk token j and query head h, for
+ * every kv head k and token t < context_lens[s]:
+ *     scores[s][k][t] += sum of p_jh[t] over the query heads h of k and the chunk's last `window` tokens j
+ *                        (every token when window is 0 or larger than the chunk).
+ * A window scores a long prompt's tokens by what its end attends to.
+ *
+ *  scores         [num_seqs][num_kv_heads][score_stride] fp32, read and written, as in
+ *                 pa_paged_attention_accumulate; entries at and past context_lens[s], and all of a sequence
+ *                 without new tokens, keep their values.
+ *  score_stride   entries between the rows, >= max_context_len.
+ *  max_context_len  >= every context_lens[s]; sizes the grid.
+ *  workspace      >= pa_paged_prefill_accumulate_workspace_size(...) bytes, its header zeroed once.
+ * Everything else is as in pa_paged_prefill. Weights are formed in fp32 from the unrounded scores. A chunk
+ * outside its context, or a length past max_context_len (PA_DEVERR_CONTEXT_LEN), leaves the sequence's scores
+ * as they are; tokens seen by a counted row that also sees a block outside the pool (PA_DEVERR_BLOCK_ID) get NaN.
+ */
+PA_API pa_status pa_paged_prefill_accumulate(void* out, float* scores, int score_stride, const void* query,
+                                             pa_dtype q_dtype, const void* key_cache, const void* value_cache,
+                                             pa_dtype kv_dtype, const float* k_scale, const float* v_scale,
+                                             const int32_t* block_tables, int max_blocks_per_seq,
+                                             const int32_t* context_lens, const int32_t* q_start, int num_seqs,
+                                             int num_q_tokens, int num_heads, int num_kv_heads, int head_size,
+                                             int block_size, int num_blocks, int max_q_len, int max_context_len,
+                                             int window, float scale, void* workspace, size_t workspace_bytes,
+                                             pa_stream_t stream);
+
+/*
+ * Workspace bytes of pa_paged_cross_attention: the header, and fp32 partial results when the keys are split
+ * over several CTAs (few query rows over long contexts). 0 if the arguments are invalid. Makes no CUDA call.
+ */
+PA_API size_t pa_paged_cross_attention_workspace_size(int num_seqs, int num_q_tokens, int num_heads,
+                                                      int num_kv_heads, int head_size, int max_q_len,
+                                                      int max_context_len);
+
+/*
+ * Cross attention: the query rows of a sequence (a decoder's text tokens) attend to the cached states of its
+ * encoder (an image, a recording), whose number context_lens[s] = E_s has nothing to do with the queries'.
+ * Every row of sequence s sees all E_s states. For rows q_start[s] .. q_start[s+1]-1 and every head h (kv head
+ * h / (num_heads / num_kv_heads)):
+ *     out[row][h][:] = softmax_{t < E_s}(scale * q . k_t) . v_t       (fp32 accumulation); 0 when E_s is 0.
+ * The states' keys and values are written once with pa_reshape_and_cache and read by prompts and decode
+ * steps alike (one row per sequence).
+ *
+ *  max_q_len        >= every q_start[s+1] - q_start[s]; max_context_len >= every E_s. Both size the grid.
+ *  workspace        >= pa_paged_cross_attention_workspace_size(...) bytes, its header zeroed once.
+ * Types, layouts and supported sizes as in pa_paged_prefill. A negative E_s, or one past the block table or
+ * past max_context_len, sets PA_DEVERR_CONTEXT_LEN and NaNs the sequence's rows; a block id outside the pool
+ * sets PA_DEVERR_BLOCK_ID.
+ */
+PA_API pa_status pa_paged_cross_attention(void* out, const void* query, pa_dtype q_dtype, const void* key_cache,
+                                          const void* value_cache, pa_dtype kv_dtype, const float* k_scale,
+                                          const float* v_scale, const int32_t* block_tables, int max_blocks_per_seq,
+                                          const int32_t* context_lens, const int32_t* q_start, int num_seqs,
+                                          int num_q_tokens, int num_heads, int num_kv_heads, int head_size,
+                                          int block_size, int num_blocks, int max_q_len, int max_context_len,
+                                          float scale, void* workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
  * Write new tokens into their physical slots ([V] "PagedAttention的破局思路": blocks are filled as the
  * sequence grows). For token i with slot = slot_mapping[i] in [0, num_blocks*block_size):
  *     key_cache[slot / block_size][slot % block_size][h][:] = key[i][h][:]   (same for value)
@@ -250,6 +348,39 @@ PA_API pa_status pa_reshape_and_cache(const void* key, const void* value, pa_dty
                                const float* k_scale, const float* v_scale,
                                const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
                                int head_size, int block_size, int num_blocks, pa_stream_t stream);
+
+/*
+ * Rotary positions with several axes, applied to new queries and keys on the way into the cache (one
+ * launch instead of a rotation pass and pa_reshape_and_cache). Pair i (i < rotary_size / 2) of a head is
+ * elements (i, i + rotary_size / 2), or (2i, 2i + 1) when interleaved is 1. With
+ *     a = positions[freq_axis[i]][token] * inv_freq[i]
+ * the pair (x, y) becomes (x cos a - y sin a, y cos a + x sin a); elements rotary_size and above pass
+ * through. One axis is the ordinary rotary embedding; image and video tokens carry one position per
+ * axis (time, height, width), and freq_axis says which axis each frequency follows. Turned queries go to
+ * query_out; turned keys and unchanged values go to their slots as in pa_reshape_and_cache (slots that are
+ * negative or past the pool are skipped for key and value, the token's query is turned all the same).
+ * Angles are reduced in 64 bits, so far positions lose nothing; rotation is in fp32 and rounded once to
+ * the output type (an FP8 key is E4M3(turned / scale), not rounded to 16 bits in between).
+ *
+ *  query_out      num_tokens rows of [num_heads][head_size], in_dtype, query_out_stride elements apart; may
+ *                 be query itself (same pointer and stride: turned in place), must not overlap it otherwise.
+ *  query          rows of [num_heads][head_size]; key, value: rows of [num_kv_heads][head_size]; in_dtype.
+ *                 Strides are elements between tokens: at least a row (slices of one fused projection
+ *                 are fine), multiples of 8.
+ *  key_cache, value_cache, k_scale, v_scale, slot_mapping   as in pa_reshape_and_cache.
+ *  positions      [num_axes][num_tokens] int32 (negative positions turn backwards).
+ *  inv_freq       [rotary_size / 2] fp32, the angle per position of each pair.
+ *  freq_axis      [rotary_size / 2] int32; a pair whose axis is outside [0, num_axes) is not turned.
+ * Supported: head_size a multiple of 8, rotary_size a multiple of 16 up to min(head_size, 512); cache dtype
+ * in_dtype, PA_FP8_E4M3 or PA_FP8_E4M3_BLOCK. num_tokens == 0 is a no-op (pointers may then be null).
+ */
+PA_API pa_status pa_rope_reshape_and_cache(
+    void* query_out, int64_t query_out_stride, const void* query, int64_t query_stride, const void* key,
+    int64_t key_stride, const void* value, int64_t value_stride, pa_dtype in_dtype, void* key_cache, void* value_cache,
+    pa_dtype kv_dtype, const float* k_scale, const float* v_scale, const int64_t* slot_mapping,
+    const int32_t* positions, int num_axes, const float* inv_freq, const int32_t* freq_axis, int rotary_size,
+    int interleaved, int num_tokens, int num_heads, int num_kv_heads, int head_size, int block_size, int num_blocks,
+    pa_stream_t stream);
 
 /*
  * Copy-on-write of shared blocks ([V] "PagedAttention的局限性"; sharing by reference count in [T]
@@ -287,6 +418,47 @@ PA_API pa_status pa_copy_blocks_layers(void* const* key_caches, void* const* val
                                        pa_dtype kv_dtype, const int64_t* block_mapping, int num_pairs,
                                        int num_kv_heads, int head_size, int block_size, int num_blocks,
                                        pa_stream_t stream);
+
+/*
+ * Eviction by accumulated attention weight: cut every sequence to at most `budget` cached tokens, keeping
+ * per kv head the tokens that attention has used most (scores as pa_paged_attention_accumulate and
+ * pa_paged_prefill_accumulate gather them). For sequence s with L = context_lens[s] tokens and kv head h:
+ * L <= budget keeps every token; otherwise the first num_sink, the last num_recent and, of the tokens
+ * between, the budget - num_sink - num_recent with the largest scores stay (equal scores: the lower index
+ * first; NaN counts as -inf). The kept tokens stay in order: token kept[s][h][j] becomes token j, its key
+ * and value row moved to offset j % block_size of block dst_block_tables[s][j / block_size]. Heads keep
+ * tokens of their own; every head of a sequence keeps min(L, budget).
+ *
+ *  kept           [num_seqs][num_kv_heads][budget] int32, written: the kept tokens' old indices, rising;
+ *                 -1 from entry min(L, budget) on.
+ *  new_lens       [num_seqs] int32, written: min(L, budget). Must not be context_lens.
+ *  scores_out     [num_seqs][num_kv_heads][score_stride] fp32, written: the kept tokens' scores, then zeros
+ *                 up to score_stride. May be scores itself (no other overlap).
+ *  scores         [num_seqs][num_kv_heads][score_stride] fp32, score_stride >= max_context_len.
+ *  key_cache,
+ *  value_cache    [num_blocks][block_size][num_kv_heads][head_size]; read and written.
+ *  block_tables   [num_seqs][max_blocks_per_seq] int32, the blocks that hold the tokens now.
+ *  dst_block_tables [num_seqs][max_dst_blocks_per_seq] int32, the blocks that hold them afterwards (the
+ *                 first ceil(min(L, budget) / block_size) entries are read). Entry i may be the sequence's
+ *                 own block_tables entry i (compaction in place; block_tables may be passed itself) if
+ *                 no other sequence reads that block; any other destination must be a block that no
+ *                 sequence of the call reads. Destinations of one call are distinct.
+ *  budget >= 1, num_sink >= 0, num_recent >= 0, num_sink + num_recent <= budget;
+ *  max_dst_blocks_per_seq * block_size >= min(budget, max_context_len).
+ *  workspace      >= PA_WORKSPACE_HEADER_BYTES, zeroed once; its first word is the device error word.
+ * Supported: kv_dtype PA_F16, PA_BF16 or PA_FP8_E4M3 (per-kv-head scales stay valid; codes with per-block
+ * scales cannot change blocks: PA_ERR_UNSUPPORTED); rows of head_size elements of 16 to 1024 bytes, a
+ * multiple of 16. A length below 0, past its table or past max_context_len sets PA_DEVERR_CONTEXT_LEN; that
+ * sequence's caches and scores stay untouched, its new length is 0 and its kept entries are -1. A block id
+ * outside the pool sets PA_DEVERR_BLOCK_ID and its rows are not moved.
+ */
+PA_API pa_status pa_evict_tokens(int32_t* kept, int32_t* new_lens, float* scores_out, const float* scores,
+                                 int score_stride, void* key_cache, void* value_cache, pa_dtype kv_dtype,
+                                 const int32_t* block_tables, int max_blocks_per_seq,
+                                 const int32_t* dst_block_tables, int max_dst_blocks_per_seq,
+                                 const int32_t* context_lens, int num_seqs, int num_kv_heads, int head_size,
+                                 int block_size, int num_blocks, int max_context_len, int budget, int num_sink,
+                                 int num_recent, void* workspace, size_t workspace_bytes, pa_stream_t stream);
 
 /*
  * Swap whole blocks between two pools ([C] "PagedAttention：把显存做成虚拟内存": pages of inactive

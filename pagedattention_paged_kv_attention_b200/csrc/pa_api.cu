@@ -18,6 +18,7 @@
 #include "pa_cache_ops.cuh"
 #include "pa_host_util.h"
 #include "pa_launch.cuh"
+#include "pa_weights.cuh"
 #include "pagedattn.h"
 
 namespace {
@@ -172,6 +173,81 @@ pa_status check_attention(const void* out, const void* query, pa_dtype q_dtype, 
   return PA_OK;
 }
 
+// The tensor maps, arguments and grid of a checked call on a workspace that is large enough.
+struct AttnLaunch {
+  CUtensorMap tk, tv;
+  pa::AttnArgs a;
+  int grid;
+};
+
+pa_status build_launch(AttnLaunch* l, const AttnPlan& plan, void* out, const void* query, const void* key_cache,
+                       const void* value_cache, pa_dtype kv_dtype, const float* k_scale, const float* v_scale,
+                       const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                       int num_heads, int num_kv_heads, int head_size, int block_size, int num_blocks, float scale,
+                       void* workspace) {
+  const int ps = plan.ps, partitions = plan.partitions, subgroups = plan.subgroups;
+  const int head_blocks = plan.head_blocks;
+  const unsigned long long items = plan.items;
+  const WorkspaceLayout& ws = plan.ws;
+  const int eb = elem_bytes(kv_dtype);
+  if (!encode_cache_map(&l->tk, key_cache, eb, head_size, num_kv_heads, block_size, num_blocks) ||
+      !encode_cache_map(&l->tv, value_cache, eb, head_size, num_kv_heads, block_size, num_blocks))
+    return PA_ERR_CUDA;
+  int device = 0, sms = 0;
+  if (cudaGetDevice(&device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || sms <= 0)
+    return PA_ERR_CUDA;
+  uint8_t* wsb = static_cast<uint8_t*>(workspace);
+  pa::AttnArgs& a = l->a;
+  a = pa::AttnArgs{};
+  a.out = out;
+  a.query = query;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.part_m = partitions > 1 ? reinterpret_cast<float*>(wsb + ws.part_m) : nullptr;
+  a.part_l = partitions > 1 ? reinterpret_cast<float*>(wsb + ws.part_l) : nullptr;
+  a.part_o = partitions > 1 ? reinterpret_cast<float*>(wsb + ws.part_o) : nullptr;
+  a.header = reinterpret_cast<unsigned int*>(wsb);
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.num_heads = num_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.group = num_heads / num_kv_heads;
+  a.subgroups = subgroups;
+  a.head_blocks = head_blocks;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.partition_size = ps;
+  a.num_partitions = partitions;
+  a.num_items = static_cast<unsigned int>(items);
+  a.scale_log2 = scale * pa::kLog2e;
+  a.scale_block_stride = scale_block_stride(kv_dtype, num_kv_heads);
+#ifdef PA_TRACE
+  a.trace = reinterpret_cast<unsigned long long*>(wsb + ws.trace);
+#endif
+  l->grid = static_cast<int>(std::min<unsigned long long>(static_cast<unsigned long long>(sms), items));
+  return PA_OK;
+}
+
+// Workspace of pa_paged_attention_accumulate: that of pa_paged_attention, then the statistics and scaled
+// scores its weights are formed from. 0 when the sizes cannot be addressed.
+struct AccumulateLayout {
+  size_t stats, logits, stride, total;
+};
+
+AccumulateLayout accumulate_layout(size_t base, int num_seqs, int num_heads, int max_context_len, int partitions) {
+  AccumulateLayout w{};
+  const size_t rows = static_cast<size_t>(num_seqs) * num_heads;
+  w.stride = round_up(static_cast<size_t>(std::max(1, max_context_len)), pa::kPartitionQuantum);
+  if (rows >= (size_t(1) << 31) || rows * w.stride >= (size_t(1) << 48)) return w;
+  w.stats = base;
+  w.logits = w.stats + round_up(rows * partitions * sizeof(float2), 256);
+  w.total = w.logits + round_up(rows * w.stride * sizeof(float), 256);
+  return w;
+}
+
 }  // namespace
 
 namespace pa_host {
@@ -240,55 +316,72 @@ pa_status pa_paged_attention(void* out, const void* query, pa_dtype q_dtype, con
   if (plan.empty) return PA_OK;  // empty batch: nothing is read or written
   if (!workspace || !aligned(workspace, 16)) return PA_ERR_INVALID_ARGUMENT;
   if (workspace_bytes < plan.ws.total) return PA_ERR_WORKSPACE_TOO_SMALL;
-  const int ps = plan.ps, partitions = plan.partitions, g_tile = plan.g_tile, subgroups = plan.subgroups;
-  const int head_blocks = plan.head_blocks;
-  const unsigned long long items = plan.items;
-  const bool fp8 = is_fp8(kv_dtype);
-  const WorkspaceLayout& ws = plan.ws;
 
   // ---- launch ----
-  CUtensorMap tk, tv;
-  const int eb = elem_bytes(kv_dtype);
-  if (!encode_cache_map(&tk, key_cache, eb, head_size, num_kv_heads, block_size, num_blocks) ||
-      !encode_cache_map(&tv, value_cache, eb, head_size, num_kv_heads, block_size, num_blocks))
-    return PA_ERR_CUDA;
-  int device = 0, sms = 0;
-  if (cudaGetDevice(&device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || sms <= 0)
-    return PA_ERR_CUDA;
-  uint8_t* wsb = static_cast<uint8_t*>(workspace);
-  pa::AttnArgs a{};
-  a.out = out;
-  a.query = query;
-  a.k_scale = k_scale;
-  a.v_scale = v_scale;
-  a.block_tables = block_tables;
-  a.context_lens = context_lens;
-  a.part_m = partitions > 1 ? reinterpret_cast<float*>(wsb + ws.part_m) : nullptr;
-  a.part_l = partitions > 1 ? reinterpret_cast<float*>(wsb + ws.part_l) : nullptr;
-  a.part_o = partitions > 1 ? reinterpret_cast<float*>(wsb + ws.part_o) : nullptr;
-  a.header = reinterpret_cast<unsigned int*>(wsb);
-  a.max_blocks_per_seq = max_blocks_per_seq;
-  a.num_seqs = num_seqs;
-  a.num_heads = num_heads;
-  a.num_kv_heads = num_kv_heads;
-  a.group = num_heads / num_kv_heads;
-  a.subgroups = subgroups;
-  a.head_blocks = head_blocks;
-  a.block_size = block_size;
-  a.num_blocks = num_blocks;
-  a.partition_size = ps;
-  a.num_partitions = partitions;
-  a.num_items = static_cast<unsigned int>(items);
-  a.scale_log2 = scale * pa::kLog2e;
-  a.scale_block_stride = scale_block_stride(kv_dtype, num_kv_heads);
-#ifdef PA_TRACE
-  a.trace = reinterpret_cast<unsigned long long*>(wsb + ws.trace);
-#endif
-  const int grid = static_cast<int>(std::min<unsigned long long>(static_cast<unsigned long long>(sms), items));
+  AttnLaunch l;
+  const pa_status built = build_launch(&l, plan, out, query, key_cache, value_cache, kv_dtype, k_scale, v_scale,
+                                       block_tables, max_blocks_per_seq, context_lens, num_seqs, num_heads,
+                                       num_kv_heads, head_size, block_size, num_blocks, scale, workspace);
+  if (built != PA_OK) return built;
+  const bool fp8 = is_fp8(kv_dtype);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = q_dtype == PA_BF16 ? pa::launch_attention_bf16(tk, tv, a, fp8, head_size, g_tile, grid, st)
-                                     : pa::launch_attention_f16(tk, tv, a, fp8, head_size, g_tile, grid, st);
+  cudaError_t e = q_dtype == PA_BF16 ? pa::launch_attention_bf16(l.tk, l.tv, l.a, fp8, head_size, plan.g_tile, l.grid, st)
+                                     : pa::launch_attention_f16(l.tk, l.tv, l.a, fp8, head_size, plan.g_tile, l.grid, st);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+size_t pa_paged_attention_accumulate_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size,
+                                                    int max_context_len, int partition_size) {
+  const size_t base = pa_paged_attention_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_context_len,
+                                                        partition_size);
+  if (base == 0) return 0;
+  const int ps = plan_partition(num_seqs, num_heads, num_kv_heads, max_context_len, partition_size);
+  return accumulate_layout(base, num_seqs, num_heads, max_context_len, std::max(1, ceil_div(max_context_len, ps))).total;
+}
+
+pa_status pa_paged_attention_accumulate(void* out, float* scores, int score_stride, const void* query,
+                                        pa_dtype q_dtype, const void* key_cache, const void* value_cache,
+                                        pa_dtype kv_dtype, const float* k_scale, const float* v_scale,
+                                        const int32_t* block_tables, int max_blocks_per_seq,
+                                        const int32_t* context_lens, int num_seqs, int num_heads, int num_kv_heads,
+                                        int head_size, int block_size, int num_blocks, int max_context_len,
+                                        float scale, int partition_size, void* workspace, size_t workspace_bytes,
+                                        pa_stream_t stream) {
+  AttnPlan plan;
+  const pa_status checked = check_attention(out, query, q_dtype, key_cache, value_cache, kv_dtype, k_scale, v_scale,
+                                            block_tables, max_blocks_per_seq, context_lens, num_seqs, num_heads,
+                                            num_kv_heads, head_size, block_size, num_blocks, max_context_len, scale,
+                                            partition_size, &plan);
+  if (checked != PA_OK) return checked;
+  if (score_stride <= 0 || score_stride < max_context_len) return PA_ERR_INVALID_ARGUMENT;
+  if (plan.empty) return PA_OK;
+  if (!scores || !aligned(scores, 4)) return PA_ERR_INVALID_ARGUMENT;
+  if (!workspace || !aligned(workspace, 16)) return PA_ERR_INVALID_ARGUMENT;
+  const AccumulateLayout w = accumulate_layout(plan.ws.total, num_seqs, num_heads, max_context_len, plan.partitions);
+  if (w.total == 0 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  if (workspace_bytes < w.total) return PA_ERR_WORKSPACE_TOO_SMALL;
+
+  AttnLaunch l;
+  const pa_status built = build_launch(&l, plan, out, query, key_cache, value_cache, kv_dtype, k_scale, v_scale,
+                                       block_tables, max_blocks_per_seq, context_lens, num_seqs, num_heads,
+                                       num_kv_heads, head_size, block_size, num_blocks, scale, workspace);
+  if (built != PA_OK) return built;
+  uint8_t* wsb = static_cast<uint8_t*>(workspace);
+  l.a.stats = reinterpret_cast<float2*>(wsb + w.stats);
+  l.a.logits = reinterpret_cast<float*>(wsb + w.logits);
+  l.a.logit_stride = static_cast<long long>(w.stride);
+  const bool fp8 = is_fp8(kv_dtype), bf16 = q_dtype == PA_BF16;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = bf16 ? pa::launch_accumulate_bf16(l.tk, l.tv, l.a, fp8, head_size, plan.g_tile, l.grid, st)
+                       : pa::launch_accumulate_f16(l.tk, l.tv, l.a, fp8, head_size, plan.g_tile, l.grid, st);
+  if (e == cudaSuccess && plan.partitions > 1)
+    e = bf16 ? pa::launch_reduce_bf16(l.a, head_size, st) : pa::launch_reduce_f16(l.a, head_size, st);
+  if (e == cudaSuccess && max_context_len > 0) {
+    const unsigned chunks = static_cast<unsigned>(ceil_div(max_context_len, pa::kWeightTokens));
+    e = pa_host::launch_overlapped(pa::attention_weights_kernel,
+                                   dim3(chunks, static_cast<unsigned>(num_kv_heads), static_cast<unsigned>(num_seqs)),
+                                   dim3(pa::kWeightThreads), 0, st, l.a, scores, static_cast<long long>(score_stride));
+  }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -103,6 +103,11 @@ struct AttnArgs {
   unsigned int num_items;       // num_partitions * num_seqs * head_blocks * subgroups
   float scale_log2;             // softmax scale * log2(e)
   int scale_block_stride;       // FP8 scales: 0 = per kv head, num_kv_heads = per (block, kv head)
+  // Weight accumulation (W instantiations only): the scaled scores z = log2(e) * scale * q.k of every
+  // token, [S][H][logit_stride], and per (s, h, partition) their max m and sum of 2^(z - m).
+  float* logits;
+  float2* stats;                // [S][H][P]
+  long long logit_stride;
   unsigned long long* trace;    // timing records, written only by builds with PA_TRACE defined (else null)
 };
 
@@ -411,7 +416,12 @@ __device__ __forceinline__ ItemCoord decode_ordered(unsigned int t, const AttnAr
 
 // BS: FP8 cache with per-(block, kv head) scales (args.scale_block_stride != 0); a separate
 // instantiation so that the per-head FP8 path carries none of its work.
-template <typename QT, typename KVT, int D, int G, bool BS>
+// W: also writes every token's scaled score and each item's softmax statistics, from which
+// attention_weights_kernel (pa_weights.cuh) forms the normalised weights. Kept apart from the plain
+// instantiations, whose code and results it leaves as they are. The sum of a W item's statistics takes
+// the weights before their rounding to 16 bits (l_run takes the rounded ones that enter P V): scores
+// accumulate over thousands of steps and carry fp32 accuracy.
+template <typename QT, typename KVT, int D, int G, bool BS, bool W = false>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                      const AttnArgs args) {
@@ -716,6 +726,8 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
     bool active = false;  // this warp's kv head exists in the current item
     float zitem = 0.f;    // per-head FP8: scale_log2 * k_scale of this warp's kv head for the item
     ItemInfo inf{};
+    float l_exact = 0.f;        // W: running sum of the unrounded weights
+    float* zrow = nullptr;      // W: this lane's place in the score row of its query head; null: no such head
 
     for (int j = 0;; ++j) {
       const int slot = j % kStages;
@@ -781,6 +793,18 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
         if (lane == 0) mbar_arrive(&qempty[qb]);
         m_run = -INFINITY;
         l_run = 0.f;
+        if constexpr (W) {
+          // Lane (g, t4) of a tensor-core tile holds tokens 2*t4 and 2*t4 + 1 of each box for head g; on the
+          // CUDA-core path (one head) lane ds of token slot tslot writes token ds * kTPI + tslot.
+          l_exact = 0.f;
+          const int g = S::kMma ? lane >> 2 : 0;
+          const long long row = static_cast<long long>(inf.s) * args.num_heads +
+                                static_cast<long long>(inf.kvh0 + cw) * args.group + inf.h_sub + g;
+          zrow = active && g < inf.heads
+                     ? args.logits + row * args.logit_stride + static_cast<long long>(inf.part) * args.partition_size +
+                           (S::kMma ? 2 * (lane & 3) : ds * S::kTPI + tslot)
+                     : nullptr;
+        }
         poisoned = false;
 #pragma unroll
         for (int g = 0; g < G; ++g)
@@ -862,15 +886,30 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
           sv[gr][1] = gr * kBoxTokens + 2 * t4 + 1 < nvalid ? sacc[gr][1] * zs[gr] : -INFINITY;
           cm = fmaxf(cm, fmaxf(sv[gr][0], sv[gr][1]));
         }
+        if constexpr (W) {
+          // Four lanes fill one 32-byte sector of a head's row. Places past the last valid token lie
+          // inside the row's padding (partitions and the stride are multiples of 64) or in the next
+          // partition's range of an uncut row, so invalid tokens are not written.
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) {
+            if (zrow && gr * kBoxTokens + 2 * t4 + 1 < nvalid)
+              *reinterpret_cast<float2*>(zrow + gr * kBoxTokens) = make_float2(sv[gr][0], sv[gr][1]);
+            else if (zrow && gr * kBoxTokens + 2 * t4 < nvalid)
+              zrow[gr * kBoxTokens] = sv[gr][0];
+          }
+          if (zrow) zrow += S::kTS;
+        }
         cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 1));
         cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 2));
         const float m_new = fmaxf(m_run, cm);
         const float alpha = fast_exp2(m_run - m_new);
         uint32_t pfrag[NG];
         float psum = 0.f;
+        if constexpr (W) l_exact *= alpha;
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
           const float p0 = fast_exp2(sv[gr][0] - m_new), p1 = fast_exp2(sv[gr][1] - m_new);
+          if constexpr (W) l_exact += p0 + p1;
           pfrag[gr] = pack2<MmaT>(p0, p1);
           // The sum uses the rounded weights that enter P V, so the weights of the output sum to one.
           const float2 pr = unpack2<MmaT>(pfrag[gr]);
@@ -983,6 +1022,15 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
           if constexpr (BS) z *= ksb[t / kBoxTokens];
           sc[it] = t < nvalid ? z : -INFINITY;
         }
+        if constexpr (W) {
+          // Every lane of a token's group holds its score: lane ds writes iteration ds's, so one store
+          // covers the stage.
+          float z = sc[0];
+#pragma unroll
+          for (int it = 1; it < S::kIters; ++it) z = ds == it ? sc[it] : z;
+          if (zrow && ds < S::kIters && ds * S::kTPI + tslot < nvalid) *zrow = z;
+          if (zrow) zrow += S::kTS;
+        }
         // ---- online softmax (per head g_lane) ----
         float cm = sc[0];
 #pragma unroll
@@ -1058,6 +1106,12 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
           if (poisoned) r = __int_as_float(0x7fc00000);
           const int h = (inf.kvh0 + cw) * args.group + inf.h_sub + g;
           const size_t rowi = (static_cast<size_t>(inf.s) * args.num_heads + h) * args.num_partitions + inf.part;
+          if constexpr (W) {
+            const unsigned quad = 0xfu << (lane & ~3);
+            float le = l_exact + __shfl_xor_sync(quad, l_exact, 1);
+            le += __shfl_xor_sync(quad, le, 2);
+            if (t4 == 0) args.stats[rowi] = make_float2(m_run, poisoned ? __int_as_float(0x7fc00000) : le);
+          }
           if (inf.write_final) {
             QT* out = static_cast<QT*>(args.out) + (static_cast<size_t>(inf.s) * args.num_heads + h) * D;
             if constexpr (EB == 2) {
@@ -1116,6 +1170,11 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
             float r = vscale / lg;
             if (poisoned) r = __int_as_float(0x7fc00000);
             const int h = (inf.kvh0 + cw) * args.group + inf.h_sub + g;
+            if constexpr (W) {
+              if (dp == 0)
+                args.stats[(static_cast<size_t>(inf.s) * args.num_heads + h) * args.num_partitions + inf.part] =
+                    make_float2(mg, poisoned ? __int_as_float(0x7fc00000) : lg);
+            }
             if (inf.write_final) {
               QT* out = static_cast<QT*>(args.out) + (static_cast<size_t>(inf.s) * args.num_heads + h) * D + dp * 8;
               *reinterpret_cast<uint2*>(out) = pack4<QT>(acc[g][0].x * r, acc[g][0].y * r, acc[g][1].x * r, acc[g][1].y * r);

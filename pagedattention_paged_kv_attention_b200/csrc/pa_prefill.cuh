@@ -50,6 +50,12 @@ constexpr uint32_t kTmemTile = 256;  // per query tile: S (and P over it) in [0,
 constexpr uint32_t kTmemO = 128;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays below 2^8 between rescales
 
+// What a launch computes. kCausal: causal attention of each chunk over its prefix. kCausalStats: the same, and
+// the log2 sum of 2^(scaled scores) of every row (pa_prefill_weights.cuh forms the weights with it). kCross:
+// every query of a sequence sees all its cached keys (an encoder's states, of another length than the
+// chunk); the keys may be split over several CTAs, whose results cross_merge_kernel joins.
+enum Mode { kCausal = 0, kCausalStats = 1, kCross = 2 };
+
 struct PrefillArgs {
   void* out;                    // [T][H][d]
   const float* k_scale;         // FP8: [Hkv] or [num_blocks][Hkv] (scale_block_stride = Hkv); else null
@@ -62,6 +68,13 @@ struct PrefillArgs {
   int max_blocks_per_seq, num_seqs, num_q_tokens, num_heads, num_kv_heads, group, tile_tokens, block_size,
       num_blocks, num_pairs;
   float scale_log2;             // scale * log2(e)
+  float* lse;                   // kCausalStats: [T][H]
+  // kCross: CTAs that share a query tile's keys, key tiles of each, and (splits > 1) their fp32 results:
+  // max and sum [T][H][splits], normalised rows [T][H][splits][d].
+  int splits, split_tiles, max_context_len;
+  float* part_m;
+  float* part_l;
+  float* part_o;
 };
 
 template <int D>
@@ -87,6 +100,7 @@ struct Bars {
   float box_scale[kStages][2][kKvTile / 8];            // per-block FP8: K and V scale of each box
   uint32_t tmem_base;
   int abort;
+  int bad_block;  // a key tile of this CTA names a block outside the pool
 };
 
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
@@ -159,7 +173,7 @@ __device__ __forceinline__ void widen_row(uint8_t* tile, const uint8_t* staged, 
 }
 
 // KVB: cache element bytes (2: a T cache; 1: E4M3). BS: E4M3 with per-(block, kv head) scales.
-template <typename T, int D, int KVB, bool BS>
+template <typename T, int D, int KVB, bool BS, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv, const PrefillArgs a) {
@@ -171,7 +185,10 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars* b = reinterpret_cast<Bars*>(sm + L::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pair = a.num_pairs - 1 - static_cast<int>(blockIdx.x);  // longest prefixes first
+  constexpr bool kIsCross = MODE == kCross;
+  const int split = kIsCross ? static_cast<int>(blockIdx.x) % a.splits : 0;
+  const int pair =
+      a.num_pairs - 1 - (kIsCross ? static_cast<int>(blockIdx.x) / a.splits : static_cast<int>(blockIdx.x));  // longest prefixes first
   const int kvh = blockIdx.y, s = blockIdx.z;
   const int G = a.group;
 
@@ -184,17 +201,20 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     if (pair == 0 && threadIdx.x == 0 && (n < 0 || q0 < 0)) atomicOr(a.error_word, PA_DEVERR_CONTEXT_LEN);
     return;
   }
-  if (n > ctx || q0 + n > a.num_q_tokens ||
-      static_cast<long long>(ctx) > static_cast<long long>(a.max_blocks_per_seq) * a.block_size) {
-    // A chunk must lie inside its context and inside the query array: flag it, NaN the rows.
-    if (threadIdx.x == 0) atomicOr(a.error_word, PA_DEVERR_CONTEXT_LEN);
-    if (threadIdx.x < kTiles * kRows && q0 + n <= a.num_q_tokens) {
+  const bool bad = (kIsCross ? ctx < 0 : n > ctx) || (MODE != kCausal && ctx > a.max_context_len) ||
+                   q0 + n > a.num_q_tokens ||
+                   static_cast<long long>(ctx) > static_cast<long long>(a.max_blocks_per_seq) * a.block_size;
+  if (bad || (kIsCross && ctx == 0)) {
+    // A chunk must lie inside its context and inside the query array: flag it, NaN the rows. Cross
+    // attention to no keys at all gives zeros.
+    if (bad && threadIdx.x == 0) atomicOr(a.error_word, PA_DEVERR_CONTEXT_LEN);
+    if (threadIdx.x < kTiles * kRows && q0 + n <= a.num_q_tokens && split == 0) {
       const int tok = tok0 + static_cast<int>(threadIdx.x) / G;
       if (tok < n) {
         T* o = static_cast<T*>(a.out) +
                (static_cast<size_t>(q0 + tok) * a.num_heads + kvh * G + threadIdx.x % G) * D;
-        const float nan = __int_as_float(0x7fc00000);
-        for (int i = 0; i < D; i += 2) *reinterpret_cast<uint32_t*>(o + i) = pack_pair<T>(nan, nan);
+        const float fill = bad ? __int_as_float(0x7fc00000) : 0.f;
+        for (int i = 0; i < D; i += 2) *reinterpret_cast<uint32_t*>(o + i) = pack_pair<T>(fill, fill);
       }
     }
     return;
@@ -202,10 +222,18 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   // Per tile: first token, KV tiles needed (0 when the tile lies past the chunk).
   int tile_tok0[kTiles], nkv_t[kTiles];
   int p_max = 0;
+  // Cross attention: this CTA's keys [key0, p_max].
+  const int key0 = kIsCross ? split * a.split_tiles * kKvTile : 0;
+  if (kIsCross) {
+    if (key0 >= ctx) return;
+    p_max = min(ctx - key0, a.split_tiles * kKvTile) + key0 - 1;
+  }
 #pragma unroll
   for (int x = 0; x < kTiles; ++x) {
     tile_tok0[x] = tok0 + x * a.tile_tokens;
-    if (tile_tok0[x] < n) {
+    if (kIsCross) {
+      nkv_t[x] = tile_tok0[x] < n ? (p_max - key0) / kKvTile + 1 : 0;
+    } else if (tile_tok0[x] < n) {
       const int pm = ctx - n + min(n, tile_tok0[x] + a.tile_tokens) - 1;  // last key the tile needs
       nkv_t[x] = pm / kKvTile + 1;
       p_max = max(p_max, pm);
@@ -213,7 +241,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       nkv_t[x] = 0;
     }
   }
-  const int nkv = p_max / kKvTile + 1;  // = nkv_t of the last active tile
+  const int nkv = (p_max - key0) / kKvTile + 1;  // = nkv_t of the last active tile
 
   // The TMA warp fetches its tensor maps and the first KV tile's block ids now, so that those loads
   // overlap the set-up below.
@@ -224,8 +252,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       tma_prefetch_desc(&tk);
       tma_prefetch_desc(&tv);
     }
-    if (lane * a.block_size < min(kKvTile, p_max + 1))
-      blk_first = __ldg(a.block_tables + static_cast<size_t>(s) * a.max_blocks_per_seq + lane);
+    if (lane * a.block_size < min(kKvTile, p_max + 1 - key0))
+      blk_first = __ldg(a.block_tables + static_cast<size_t>(s) * a.max_blocks_per_seq + key0 / a.block_size + lane);
   }
 
   // ---- set-up: barriers (thread 0), TMEM (warp 1) ----
@@ -247,6 +275,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     }
     mbar_init(&b->mma_done, 1);
     b->abort = 0;
+    b->bad_block = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -275,7 +304,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     // read it, long before the PV MMAs release the V slot, so the next K arrives early.
     for (int j = 0; j < nkv; ++j) {
       const int stage = j % kStages;
-      const int first = j * kKvTile;
+      const int first = key0 + j * kKvTile;
       const int ntok = min(kKvTile, p_max + 1 - first);
       const int nblk = (ntok + bs - 1) / bs;
       int blk = 0;
@@ -286,6 +315,10 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         if (!ok) atomicOr(err, PA_DEVERR_BLOCK_ID);
       }
       const unsigned okmask = __ballot_sync(0xffffffffu, ok);
+      if constexpr (MODE == kCausalStats) {
+        if (lane < nblk && !ok) *reinterpret_cast<volatile int*>(&b->bad_block) = 1;
+        __syncwarp();  // published by the arrival on the tile's barrier
+      }
       const uint32_t bytes = __popc(okmask) * bs * 128 * (kFp8 ? 1 : L::kChunks);
       uint8_t* st = sm + L::kKV + stage * L::kStage;
       bool go = true;
@@ -364,7 +397,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           const int r = ct + 64 * h;
           __half2 sc = __float2half2_rn(1.f);
           if constexpr (BS) {
-            if (j * kKvTile + r <= p_max) sc = __float2half2_rn(b->box_scale[stage][part][r / a.block_size]);
+            if (key0 + j * kKvTile + r <= p_max) sc = __float2half2_rn(b->box_scale[stage][part][r / a.block_size]);
           }
           widen_row(tile, tile + kKvTile * 128, r, sc, BS);
         }
@@ -411,7 +444,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       if (j == nkv - 1) {
         // Keys past the last one any row needs (not loaded, or past the context) must not reach PV
         // as stale or NaN values: zero those V rows of the last tile before its PV MMAs.
-        const int cut = p_max + 1 - j * kKvTile;
+        const int cut = p_max + 1 - key0 - j * kKvTile;
         if (cut < kKvTile) {
           uint8_t* vb = sm + L::kKV + (j % kStages) * L::kStage + L::kV;
           const int units = (kKvTile - cut) * 8;
@@ -460,7 +493,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     if (nkv_x > 0) {
       const int tok = tile_tok0[x] + r / G;
       const bool row_valid = tok < n;
-      const int pos = ctx - n + min(tok, n - 1);    // rows past the chunk reuse its last position
+      // Last key the row sees; rows past the chunk reuse its last position.
+      const int pos = kIsCross ? p_max : ctx - n + min(tok, n - 1);
       const int pos_lane0 = __shfl_sync(0xffffffffu, pos, 0);
       const uint32_t t_s = tmem + x * kTmemTile + (static_cast<uint32_t>(r & ~31) << 16);
       const uint32_t t_o = t_s + kTmemO;
@@ -472,7 +506,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       for (int j = 0; j < nkv_x; ++j) {
         if (!(ok = warp_wait_or_abort(b, &b->s_full[x], j & 1, err))) break;
         tc_fence_after();
-        const int base = j * kKvTile;
+        const int base = key0 + j * kKvTile;
         // The whole S row at once: four loads in flight, then one wait.
         uint32_t v[kKvTile / 32][32];
 #pragma unroll
@@ -546,20 +580,51 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       if (ok) {
         tc_fence_after();
         const float inv = out_scale / l;
-        T* dst = static_cast<T*>(a.out) + (static_cast<size_t>(q0 + min(tok, n - 1)) * a.num_heads + kvh * G + r % G) * D;
+        const size_t rowi = static_cast<size_t>(q0 + min(tok, n - 1)) * a.num_heads + kvh * G + r % G;
+        if constexpr (MODE == kCausalStats) {
+          // A tile that could not be read leaves its rows no statistics (and the weights no value).
+          if (row_valid)
+            a.lse[rowi] = *reinterpret_cast<volatile int*>(&b->bad_block) ? __int_as_float(0x7fc00000) : m + log2f(l);
+        }
+        if constexpr (kIsCross) {
+          if (ctx > a.split_tiles * kKvTile) {  // this sequence's keys are shared by several CTAs
+            float* po = a.part_o + (rowi * a.splits + split) * D;
+            if (row_valid) {
+              a.part_m[rowi * a.splits + split] = m;
+              a.part_l[rowi * a.splits + split] = l;
+            }
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t v[32];
-          tmem_ld32(t_o + 32 * c, v);
-          tmem_wait_ld(v);
-          if (row_valid) {
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[32];
+              tmem_ld32(t_o + 32 * c, v);
+              tmem_wait_ld(v);
+              if (row_valid) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              *reinterpret_cast<uint4*>(dst + 32 * c + i) = make_uint4(
-                  pack_pair<T>(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv),
-                  pack_pair<T>(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv),
-                  pack_pair<T>(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv),
-                  pack_pair<T>(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv));
+                for (int i = 0; i < 32; i += 4)
+                  *reinterpret_cast<float4*>(po + 32 * c + i) =
+                      make_float4(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv,
+                                  __uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
+              }
+            }
+            ok = false;  // stored
+          }
+        }
+        if (ok) {
+          T* dst = static_cast<T*>(a.out) + rowi * D;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            tmem_ld32(t_o + 32 * c, v);
+            tmem_wait_ld(v);
+            if (row_valid) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4*>(dst + 32 * c + i) = make_uint4(
+                    pack_pair<T>(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv),
+                    pack_pair<T>(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv),
+                    pack_pair<T>(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv),
+                    pack_pair<T>(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv));
+            }
           }
         }
       }

@@ -27,6 +27,9 @@ EXPORTS = (
     "pa_reshape_and_cache", "pa_copy_blocks", "pa_copy_blocks_check", "pa_get_device_error",
     "pa_clear_device_error", "pa_status_string", "pa_paged_attention_static", "pa_selftest_wait_timeout",
     "pa_swap_blocks", "pa_reshape_and_cache_layers", "pa_copy_blocks_layers", "pa_paged_prefill",
+    "pa_rope_reshape_and_cache", "pa_evict_tokens", "pa_paged_attention_accumulate_workspace_size",
+    "pa_paged_attention_accumulate", "pa_paged_prefill_accumulate_workspace_size", "pa_paged_prefill_accumulate",
+    "pa_paged_cross_attention_workspace_size", "pa_paged_cross_attention",
     # include/pa_block_manager.h
     "pa_bm_create", "pa_bm_destroy", "pa_bm_add_sequence", "pa_bm_fork", "pa_bm_append_slots",
     "pa_bm_block_tables", "pa_bm_plan_decode", "pa_bm_free_sequence", "pa_bm_swap_out", "pa_bm_swap_in",
@@ -50,6 +53,11 @@ lib.pa_paged_attention_workspace_size.argtypes = [_i, _i, _i, _i, _i, _i]
 lib.pa_paged_attention.restype = _i
 lib.pa_paged_attention.argtypes = [_p, _p, _i, _p, _p, _i, _p, _p, _p, _i, _p, _i, _i, _i, _i, _i, _i, _i, _f,
                                    _i, _p, _sz, _p]
+lib.pa_paged_attention_accumulate_workspace_size.restype = _sz
+lib.pa_paged_attention_accumulate_workspace_size.argtypes = [_i, _i, _i, _i, _i, _i]
+lib.pa_paged_attention_accumulate.restype = _i
+lib.pa_paged_attention_accumulate.argtypes = [_p, _p, _i, _p, _i, _p, _p, _i, _p, _p, _p, _i, _p, _i, _i, _i, _i, _i,
+                                              _i, _i, _f, _i, _p, _sz, _p]
 lib.pa_paged_attention_static.restype = _i
 lib.pa_paged_attention_static.argtypes = [_p, _p, _i, _p, _p, _i, _p, _p, _p, _i, _p, _i, _i, _i, _i, _i, _i, _i,
                                           _f, _i, _p, _p]
@@ -60,6 +68,16 @@ lib.pa_probe_paged_read.argtypes = [_p, _p, _i, _p, _i, _p, _i, _i, _i, _i, _i, 
 lib.pa_paged_prefill.restype = _i
 lib.pa_paged_prefill.argtypes = [_p, _p, _i, _p, _p, _i, _p, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f,
                                  _p, _sz, _p]
+lib.pa_paged_prefill_accumulate_workspace_size.restype = _sz
+lib.pa_paged_prefill_accumulate_workspace_size.argtypes = [_i, _i]
+lib.pa_paged_prefill_accumulate.restype = _i
+lib.pa_paged_prefill_accumulate.argtypes = [_p, _p, _i, _p, _i, _p, _p, _i, _p, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i,
+                                            _i, _i, _i, _i, _i, _f, _p, _sz, _p]
+lib.pa_paged_cross_attention_workspace_size.restype = _sz
+lib.pa_paged_cross_attention_workspace_size.argtypes = [_i] * 7
+lib.pa_paged_cross_attention.restype = _i
+lib.pa_paged_cross_attention.argtypes = [_p, _p, _i, _p, _p, _i, _p, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i,
+                                         _i, _f, _p, _sz, _p]
 lib.pa_reshape_and_cache.restype = _i
 lib.pa_reshape_and_cache.argtypes = [_p, _p, _i, _p, _p, _i, _p, _p, _p, _i, _i, _i, _i, _i, _p]
 lib.pa_copy_blocks.restype = _i
@@ -69,6 +87,12 @@ lib.pa_reshape_and_cache_layers.argtypes = [_p, _p, _i, _p, _p, _i, _p, _p, _p, 
 lib.pa_copy_blocks_layers.restype = _i
 lib.pa_copy_blocks_layers.argtypes = [_p, _p, _i, _i, _p, _i, _i, _i, _i, _i, _p]
 _i64 = ctypes.c_int64
+lib.pa_rope_reshape_and_cache.restype = _i
+lib.pa_rope_reshape_and_cache.argtypes = [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _i, _p, _p, _i, _p, _p, _p, _p, _i,
+                                          _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _p]
+lib.pa_evict_tokens.restype = _i
+lib.pa_evict_tokens.argtypes = [_p, _p, _p, _p, _i, _p, _p, _i, _p, _i, _p, _i, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i,
+                                _p, _sz, _p]
 _ip = ctypes.POINTER(ctypes.c_int)
 _i64p = ctypes.POINTER(ctypes.c_int64)
 lib.pa_bm_create.restype = _i
@@ -170,6 +194,19 @@ def _same(a, b, what):
         raise ValueError(f"{what}: shapes/dtypes differ ({tuple(a.shape)} {a.dtype} vs {tuple(b.shape)} {b.dtype})")
 
 
+def _scales(t, name, cache):
+    """The pointer of an FP8 cache's scales: [Hkv], or [num_blocks, Hkv] for per-block scales."""
+    if t is not None and tuple(t.shape) not in ((cache.shape[2],), (cache.shape[0], cache.shape[2])):
+        raise ValueError(f"{name}: expected ({cache.shape[2]},) or ({cache.shape[0]}, {cache.shape[2]}), got "
+                         f"{tuple(t.shape)}")
+    return _arg(t, name, _F32, (1, 2))
+
+
+def _same_scales(k_scale, v_scale):
+    if (k_scale is None) != (v_scale is None) or (k_scale is not None and k_scale.shape != v_scale.shape):
+        raise ValueError("k_scale/v_scale: both or neither, of one shape")
+
+
 def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -212,6 +249,57 @@ def paged_attention(out, query, key_cache, value_cache, block_tables, context_le
     return out
 
 
+def _check_batch(out, scores, query, key_cache, value_cache, block_tables, context_lens, k_scale, v_scale):
+    """The shapes that must agree in a call over a batch of S sequences (scores: [S, Hkv, stride] or None)."""
+    S, Hkv = context_lens.shape[0], key_cache.shape[2]
+    _same(out, query, "out/query")
+    _same(key_cache, value_cache, "key_cache/value_cache")
+    _same_scales(k_scale, v_scale)
+    if query.dim() != 3 or query.shape[2] != key_cache.shape[3]:
+        raise ValueError(f"query: expected [rows, heads, {key_cache.shape[3]}], got {tuple(query.shape)}")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError(f"block_tables: expected {S} rows, got {tuple(block_tables.shape)}")
+    if scores is not None and (scores.dim() != 3 or tuple(scores.shape[:2]) != (S, Hkv)):
+        raise ValueError(f"scores: expected ({S}, {Hkv}, stride), got {tuple(scores.shape)}")
+
+
+def accumulate_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_context_len, partition_size=0) -> int:
+    return lib.pa_paged_attention_accumulate_workspace_size(num_seqs, num_heads, num_kv_heads, head_size,
+                                                            max_context_len, partition_size)
+
+
+def make_accumulate_workspace(num_seqs, num_heads, num_kv_heads, head_size, max_context_len, partition_size=0,
+                              device="cuda") -> torch.Tensor:
+    """A zeroed workspace for paged_attention_accumulate (paged_attention of these sizes may share it)."""
+    n = accumulate_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_context_len, partition_size)
+    if n == 0:
+        raise ValueError("invalid sizes for a workspace")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def paged_attention_accumulate(out, scores, query, key_cache, value_cache, block_tables, context_lens, scale,
+                               max_context_len, workspace, k_scale=None, v_scale=None, partition_size=0, stream=None):
+    """paged_attention that also adds each cached token's attention weights, summed over the query heads of
+    its kv head, to scores[S,Hkv,stride] (float32)."""
+    S, H, d = query.shape
+    NB, bs, Hkv, _ = key_cache.shape
+    _check_batch(out, scores, query, key_cache, value_cache, block_tables, context_lens, k_scale, v_scale)
+    if context_lens.shape[0] != S:
+        raise ValueError(f"context_lens: expected {S} lengths, got {context_lens.shape[0]}")
+    args = (_arg(out, "out"), _arg(scores, "scores", _F32, 3), scores.shape[2], _arg(query, "query"),
+            dtype_code(query.dtype), _arg(key_cache, "key_cache"), _arg(value_cache, "value_cache"),
+            cache_code(key_cache, k_scale), _scales(k_scale, "k_scale", key_cache), _scales(v_scale, "v_scale", key_cache),
+            _arg(block_tables, "block_tables", _I32, 2), block_tables.shape[1],
+            _arg(context_lens, "context_lens", _I32, 1), S, H, Hkv, d, bs, NB, int(max_context_len), float(scale),
+            int(partition_size), _arg(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+            _stream(stream))
+    _on_current_device(out=out, scores=scores, query=query, key_cache=key_cache, value_cache=value_cache,
+                       block_tables=block_tables, context_lens=context_lens, workspace=workspace, k_scale=k_scale,
+                       v_scale=v_scale)
+    _check(lib.pa_paged_attention_accumulate(*args), "pa_paged_attention_accumulate")
+    return out
+
+
 def paged_prefill(out, query, key_cache, value_cache, block_tables, context_lens, q_start, scale, max_q_len,
                   workspace, k_scale=None, v_scale=None, stream=None):
     """Causal prefill: out[T,H,d] for query chunks query[T,H,d] (rows q_start[s]..q_start[s+1]-1 of
@@ -230,6 +318,73 @@ def paged_prefill(out, query, key_cache, value_cache, block_tables, context_lens
                               int(max_q_len), float(scale), _arg(workspace, "workspace"),
                               workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "pa_paged_prefill")
+
+
+def _check_chunks(q_start, S):
+    if q_start.dim() != 1 or q_start.shape[0] != S + 1:
+        raise ValueError(f"q_start: expected {S + 1} entries, got shape {tuple(q_start.shape)}")
+
+
+def make_prefill_accumulate_workspace(num_q_tokens, num_heads, device="cuda") -> torch.Tensor:
+    """A zeroed workspace for paged_prefill_accumulate of up to num_q_tokens query tokens."""
+    n = lib.pa_paged_prefill_accumulate_workspace_size(num_q_tokens, num_heads)
+    if n == 0:
+        raise ValueError("invalid sizes for a workspace")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def paged_prefill_accumulate(out, scores, query, key_cache, value_cache, block_tables, context_lens, q_start, scale,
+                             max_q_len, max_context_len, workspace, window=0, k_scale=None, v_scale=None, stream=None):
+    """paged_prefill that also adds the attention weights of each chunk's last `window` tokens (0: all of
+    them), summed over the query heads of each kv head, to scores[S,Hkv,stride] (float32)."""
+    T, H, d = query.shape
+    NB, bs, Hkv, _ = key_cache.shape
+    S = context_lens.shape[0]
+    _check_batch(out, scores, query, key_cache, value_cache, block_tables, context_lens, k_scale, v_scale)
+    _check_chunks(q_start, S)
+    args = (_arg(out, "out"), _arg(scores, "scores", _F32, 3), scores.shape[2], _arg(query, "query"),
+            dtype_code(query.dtype), _arg(key_cache, "key_cache"), _arg(value_cache, "value_cache"),
+            cache_code(key_cache, k_scale), _scales(k_scale, "k_scale", key_cache), _scales(v_scale, "v_scale", key_cache),
+            _arg(block_tables, "block_tables", _I32, 2), block_tables.shape[1],
+            _arg(context_lens, "context_lens", _I32, 1), _arg(q_start, "q_start", _I32, 1), S, T, H, Hkv, d, bs, NB,
+            int(max_q_len), int(max_context_len), int(window), float(scale), _arg(workspace, "workspace"),
+            workspace.numel() * workspace.element_size(), _stream(stream))
+    _on_current_device(out=out, scores=scores, query=query, key_cache=key_cache, value_cache=value_cache,
+                       block_tables=block_tables, context_lens=context_lens, q_start=q_start, workspace=workspace,
+                       k_scale=k_scale, v_scale=v_scale)
+    _check(lib.pa_paged_prefill_accumulate(*args), "pa_paged_prefill_accumulate")
+    return out
+
+
+def make_cross_workspace(num_seqs, num_q_tokens, num_heads, num_kv_heads, head_size, max_q_len, max_context_len,
+                         device="cuda") -> torch.Tensor:
+    """A zeroed workspace for paged_cross_attention of these sizes."""
+    n = lib.pa_paged_cross_attention_workspace_size(num_seqs, num_q_tokens, num_heads, num_kv_heads, head_size,
+                                                    max_q_len, max_context_len)
+    if n == 0:
+        raise ValueError("invalid sizes for a workspace")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def paged_cross_attention(out, query, key_cache, value_cache, block_tables, context_lens, q_start, scale, max_q_len,
+                          max_context_len, workspace, k_scale=None, v_scale=None, stream=None):
+    """Cross attention: rows q_start[s]..q_start[s+1]-1 of query[T,H,d] attend to all context_lens[s] cached
+    states of sequence s's encoder (no causal mask; zeros where there are none)."""
+    T, H, d = query.shape
+    NB, bs, Hkv, _ = key_cache.shape
+    S = context_lens.shape[0]
+    _check_batch(out, None, query, key_cache, value_cache, block_tables, context_lens, k_scale, v_scale)
+    _check_chunks(q_start, S)
+    args = (_arg(out, "out"), _arg(query, "query"), dtype_code(query.dtype), _arg(key_cache, "key_cache"),
+            _arg(value_cache, "value_cache"), cache_code(key_cache, k_scale), _scales(k_scale, "k_scale", key_cache),
+            _scales(v_scale, "v_scale", key_cache), _arg(block_tables, "block_tables", _I32, 2), block_tables.shape[1],
+            _arg(context_lens, "context_lens", _I32, 1), _arg(q_start, "q_start", _I32, 1), S, T, H, Hkv, d, bs, NB,
+            int(max_q_len), int(max_context_len), float(scale), _arg(workspace, "workspace"),
+            workspace.numel() * workspace.element_size(), _stream(stream))
+    _on_current_device(out=out, query=query, key_cache=key_cache, value_cache=value_cache, block_tables=block_tables,
+                       context_lens=context_lens, q_start=q_start, workspace=workspace, k_scale=k_scale, v_scale=v_scale)
+    _check(lib.pa_paged_cross_attention(*args), "pa_paged_cross_attention")
+    return out
 
 
 def paged_attention_static(out, query, key_cache, value_cache, block_tables, context_lens, scale,
@@ -265,6 +420,99 @@ def reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, k_scale=
                                   _arg(v_scale, "v_scale", _F32, (1, 2)),
                                   _arg(slot_mapping, "slot_mapping", _I64, 1), T, Hkv, d, bs, NB, _stream(stream))
     _check(st, "pa_reshape_and_cache")
+
+
+def _on_current_device(**tensors):
+    """Every tensor is on the current device: the kernels run there, on its current stream."""
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+
+
+def _token_rows(t, name, dtype):
+    """Pointer and token stride of a [T, heads, d] tensor whose tokens are dense rows, possibly further
+    apart than a row (a slice of a fused projection)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dim() != 3 or t.dtype != dtype:
+        raise ValueError(f"{name}: expected 3 dimensions of {dtype}, got shape {tuple(t.shape)} {t.dtype}")
+    T, H, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: each token's [heads, head_size] row must be dense, got strides {t.stride()}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if T > 1 else H * d)
+
+
+def rope_reshape_and_cache(query_out, query, key, value, key_cache, value_cache, slot_mapping, positions, inv_freq,
+                           freq_axis, interleaved=False, k_scale=None, v_scale=None, stream=None):
+    """Turn query[T,H,d] into query_out and key[T,Hkv,d] into its cache slots by rotary positions with
+    several axes (positions[A,T] int32; inv_freq[R/2] float32; freq_axis[R/2] int32, the axis each
+    frequency follows), and write value beside the keys. Token rows may be strided (slices of a fused
+    projection); query_out may be query."""
+    T, H, d = query.shape
+    NB, bs, Hkv, d2 = key_cache.shape
+    _same(key_cache, value_cache, "key_cache/value_cache")
+    if query_out.shape != query.shape:
+        raise ValueError(f"query_out/query: shapes differ ({tuple(query_out.shape)} vs {tuple(query.shape)})")
+    if key.shape != (T, Hkv, d2) or value.shape != (T, Hkv, d2) or d2 != d:
+        raise ValueError(f"key/value: expected {(T, Hkv, d)}, got {tuple(key.shape)} and {tuple(value.shape)}")
+    if positions.dim() != 2 or positions.shape[1] != T or slot_mapping.shape != (T,):
+        raise ValueError(f"positions/slot_mapping: expected [axes, {T}] and [{T}], got {tuple(positions.shape)} and "
+                         f"{tuple(slot_mapping.shape)}")
+    if inv_freq.shape != freq_axis.shape:
+        raise ValueError(f"inv_freq/freq_axis: lengths differ ({tuple(inv_freq.shape)} vs {tuple(freq_axis.shape)})")
+    _same_scales(k_scale, v_scale)
+    rows = [x for t, name in ((query_out, "query_out"), (query, "query"), (key, "key"), (value, "value"))
+            for x in _token_rows(t, name, query.dtype)]
+    args = (*rows, dtype_code(query.dtype), _arg(key_cache, "key_cache"), _arg(value_cache, "value_cache"),
+            cache_code(key_cache, k_scale), _scales(k_scale, "k_scale", key_cache), _scales(v_scale, "v_scale", key_cache),
+            _arg(slot_mapping, "slot_mapping", _I64, 1), _arg(positions, "positions", _I32, 2), positions.shape[0],
+            _arg(inv_freq, "inv_freq", _F32, 1), _arg(freq_axis, "freq_axis", _I32, 1), 2 * inv_freq.shape[0],
+            int(bool(interleaved)), T, H, Hkv, d, bs, NB, _stream(stream))
+    _on_current_device(query_out=query_out, query=query, key=key, value=value, key_cache=key_cache,
+                       value_cache=value_cache, slot_mapping=slot_mapping, positions=positions, inv_freq=inv_freq,
+                       freq_axis=freq_axis, k_scale=k_scale, v_scale=v_scale)
+    _check(lib.pa_rope_reshape_and_cache(*args), "pa_rope_reshape_and_cache")
+    return query_out
+
+
+def make_evict_workspace(device="cuda") -> torch.Tensor:
+    """A zeroed workspace for evict_tokens (its error word)."""
+    return torch.zeros(WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=device)
+
+
+def evict_tokens(kept, new_lens, scores_out, scores, key_cache, value_cache, block_tables, dst_block_tables,
+                 context_lens, budget, num_sink, num_recent, max_context_len, workspace, k_scale=None, stream=None):
+    """Cut every sequence to at most `budget` tokens: per kv head the first num_sink, the last num_recent
+    and the highest scores[S,Hkv,stride] between them stay, moved together in order into the blocks of
+    dst_block_tables (block_tables itself: in place). Writes kept[S,Hkv,budget], new_lens[S] and
+    scores_out. Per-block FP8 scales (a 2-D k_scale) are refused: their codes cannot change blocks."""
+    NB, bs, Hkv, d = key_cache.shape
+    S = context_lens.shape[0]
+    _same(key_cache, value_cache, "key_cache/value_cache")
+    _same(scores_out, scores, "scores_out/scores")
+    if scores.dim() != 3 or tuple(scores.shape[:2]) != (S, Hkv):
+        raise ValueError(f"scores: expected ({S}, {Hkv}, stride), got {tuple(scores.shape)}")
+    if tuple(kept.shape) != (S, Hkv, int(budget)) or tuple(new_lens.shape) != (S,):
+        raise ValueError(f"kept/new_lens: expected {(S, Hkv, int(budget))} and {(S,)}, got {tuple(kept.shape)} and "
+                         f"{tuple(new_lens.shape)}")
+    if block_tables.dim() != 2 or dst_block_tables.dim() != 2 or block_tables.shape[0] != S or \
+            dst_block_tables.shape[0] != S:
+        raise ValueError(f"block tables: expected {S} rows, got {tuple(block_tables.shape)} and "
+                         f"{tuple(dst_block_tables.shape)}")
+    args = (_arg(kept, "kept", _I32, 3), _arg(new_lens, "new_lens", _I32, 1), _arg(scores_out, "scores_out", _F32, 3),
+            _arg(scores, "scores", _F32, 3), scores.shape[2], _arg(key_cache, "key_cache"),
+            _arg(value_cache, "value_cache"), cache_code(key_cache, k_scale), _arg(block_tables, "block_tables", _I32, 2),
+            block_tables.shape[1], _arg(dst_block_tables, "dst_block_tables", _I32, 2), dst_block_tables.shape[1],
+            _arg(context_lens, "context_lens", _I32, 1), S, Hkv, d, bs, NB, int(max_context_len), int(budget),
+            int(num_sink), int(num_recent), _arg(workspace, "workspace"),
+            workspace.numel() * workspace.element_size(), _stream(stream))
+    _on_current_device(kept=kept, new_lens=new_lens, scores_out=scores_out, scores=scores, key_cache=key_cache,
+                       value_cache=value_cache, block_tables=block_tables, dst_block_tables=dst_block_tables,
+                       context_lens=context_lens, workspace=workspace)
+    _check(lib.pa_evict_tokens(*args), "pa_evict_tokens")
 
 
 def copy_blocks(key_cache, value_cache, block_mapping, stream=None):
