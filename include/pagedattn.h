@@ -151,7 +151,7 @@ PA_API pa_status pa_paged_attention(void* out, const void* query, pa_dtype q_dty
                              void* workspace, size_t workspace_bytes, pa_stream_t stream);
 
 /*
- * Workspace bytes of pa_paged_attention_accumulate: pa_paged_attention_workspace_size(...) plus the scaled
+ * Workspace bytes of pa_paged_attention_accumulate: pa_paged_attention_workspace_size(...) at its partition size, plus the scaled
  * scores of the step, 4 * num_seqs * num_heads * round_up(max_context_len, 64) bytes, and softmax statistics
  * of 8 bytes per (sequence, head, partition). Returns 0 if the arguments are invalid. Makes no CUDA call.
  */
@@ -160,14 +160,15 @@ PA_API size_t pa_paged_attention_accumulate_workspace_size(int num_seqs, int num
 
 /*
  * pa_paged_attention that also adds the step's attention weights to the cached tokens' scores, the
- * statistic that pa_evict_tokens evicts by. out is pa_paged_attention's, bit for bit, and with p_h its
- * softmax weights of query head h, for every kv head k and token t < context_lens[s]:
+ * statistic that pa_evict_tokens evicts by. out is pa_paged_attention's (bit for bit at one partition size),
+ * and with p_h its softmax weights of query head h, for every kv head k and token t < context_lens[s]:
  *     scores[s][k][t] += sum of p_h[t] over the num_heads / num_kv_heads query heads h of k.
  *
  *  scores         [num_seqs][num_kv_heads][score_stride] fp32, read and written; row s belongs to sequence s
  *                 of this batch (a token's entry starts at zero when the token is appended). Entries at and
  *                 past context_lens[s] are neither read nor written.
  *  score_stride   entries between the rows, >= max_context_len.
+ *  partition_size 0 = library's choice, which is finer than pa_paged_attention's for batches of few items.
  *  workspace      >= pa_paged_attention_accumulate_workspace_size(...); otherwise as pa_paged_attention's,
  *                 and both calls may share it in stream order.
  * Everything else is as in pa_paged_attention. Weights are formed in fp32 from the unrounded scores. A block

@@ -21,7 +21,8 @@ LIBRARY = os.path.join(HERE, "libpagedattn.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 SOURCES = ["pa_api.cu", "pa_attention_bf16.cu", "pa_attention_f16.cu", "pa_static_workspace.cu",
-           "pa_prefill.cu", "pa_accumulate_bf16.cu", "pa_accumulate_f16.cu", "pa_prefill_accumulate.cu", "pa_cross.cu",
+           "pa_prefill.cu", "pa_accumulate_bf16.cu", "pa_accumulate_f16.cu", "pa_rows_bf16.cu", "pa_rows_f16.cu",
+           "pa_prefill_accumulate.cu", "pa_cross.cu",
            "pa_rope.cu", "pa_evict.cu", "pa_probe.cu", "pa_block_manager.cpp"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

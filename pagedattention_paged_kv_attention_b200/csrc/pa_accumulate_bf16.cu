@@ -4,7 +4,7 @@
 namespace pa {
 cudaError_t launch_accumulate_bf16(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, bool fp8_cache,
                                   int D, int G, int grid, cudaStream_t stream) {
-  if (fp8_cache) return launch_attention<__nv_bfloat16, __nv_fp8_e4m3, true>(tk, tv, a, D, G, grid, stream);
-  return launch_attention<__nv_bfloat16, __nv_bfloat16, true>(tk, tv, a, D, G, grid, stream);
+  if (fp8_cache) return launch_attention<__nv_bfloat16, __nv_fp8_e4m3, kDecodeWeights>(tk, tv, a, D, G, grid, stream);
+  return launch_attention<__nv_bfloat16, __nv_bfloat16, kDecodeWeights>(tk, tv, a, D, G, grid, stream);
 }
 }  // namespace pa

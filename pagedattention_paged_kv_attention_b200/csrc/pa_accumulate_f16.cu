@@ -4,7 +4,7 @@
 namespace pa {
 cudaError_t launch_accumulate_f16(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, bool fp8_cache,
                                   int D, int G, int grid, cudaStream_t stream) {
-  if (fp8_cache) return launch_attention<__half, __nv_fp8_e4m3, true>(tk, tv, a, D, G, grid, stream);
-  return launch_attention<__half, __half, true>(tk, tv, a, D, G, grid, stream);
+  if (fp8_cache) return launch_attention<__half, __nv_fp8_e4m3, kDecodeWeights>(tk, tv, a, D, G, grid, stream);
+  return launch_attention<__half, __half, kDecodeWeights>(tk, tv, a, D, G, grid, stream);
 }
 }  // namespace pa

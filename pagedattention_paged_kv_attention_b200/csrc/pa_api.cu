@@ -231,6 +231,22 @@ pa_status build_launch(AttnLaunch* l, const AttnPlan& plan, void* out, const voi
   return PA_OK;
 }
 
+// The partition size of the calls with their own workspaces when the caller leaves it open: plan_partition's,
+// or less when that leaves SMs without an item -- then as many partitions as give every SM one, of at least
+// kPartitionQuantum tokens. A batch of one reads 8 kv heads x 256 tokens through one SM otherwise, at a
+// fortieth of the card's bandwidth (one sequence of 701 tokens: 44 us; in partitions of 64: 18 us).
+int plan_fine_partition(int num_seqs, int num_heads, int num_kv_heads, int max_context_len, int partition_size) {
+  const int ps = plan_partition(num_seqs, num_heads, num_kv_heads, max_context_len, partition_size);
+  if (ps <= 0 || partition_size > 0 || num_seqs == 0 || max_context_len == 0) return ps;
+  int g_tile, subgroups;
+  group_tiling(num_heads / num_kv_heads, &g_tile, &subgroups);
+  const long long units = static_cast<long long>(num_seqs) * ceil_div(num_kv_heads, pa::kHeadBlock) * subgroups;
+  const long long parts = kPlanSMs / units;
+  if (parts <= ceil_div(max_context_len, ps)) return ps;
+  const long long fine = (max_context_len + parts - 1) / parts;
+  return std::min(ps, static_cast<int>(round_up(static_cast<size_t>(fine), pa::kPartitionQuantum)));
+}
+
 // Workspace of pa_paged_attention_accumulate: that of pa_paged_attention, then the statistics and scaled
 // scores its weights are formed from. 0 when the sizes cannot be addressed.
 struct AccumulateLayout {
@@ -266,6 +282,42 @@ pa_status paged_attention_check(const void* out, const void* query, pa_dtype q_d
   *workspace_bytes = plan.ws.total;
   *empty = plan.empty;
   return st;
+}
+
+size_t decode_rows_workspace(int num_seqs, int num_heads, int num_kv_heads, int head_size, int max_context_len) {
+  const int ps = plan_fine_partition(num_seqs, num_heads, num_kv_heads, max_context_len, 0);
+  return ps <= 0 ? 0
+                 : pa_paged_attention_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_context_len, ps);
+}
+
+bool decode_rows_supported(int block_size, int num_blocks) {
+  return supported_block_size(block_size) && num_blocks < (1 << 27);
+}
+
+pa_status decode_rows(void* out, const void* query, pa_dtype q_dtype, const void* key_cache, const void* value_cache,
+                      pa_dtype kv_dtype, const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                      int max_blocks_per_seq, const int32_t* context_lens, const int32_t* q_start, int num_seqs,
+                      int num_q_tokens, int num_heads, int num_kv_heads, int head_size, int block_size, int num_blocks,
+                      int max_context_len, float scale, void* workspace, pa_stream_t stream) {
+  AttnPlan plan;
+  const pa_status checked = check_attention(
+      out, query, q_dtype, key_cache, value_cache, kv_dtype, k_scale, v_scale, block_tables, max_blocks_per_seq,
+      context_lens, num_seqs, num_heads, num_kv_heads, head_size, block_size, num_blocks, max_context_len, scale,
+      plan_fine_partition(num_seqs, num_heads, num_kv_heads, max_context_len, 0), &plan);
+  if (checked != PA_OK || plan.empty) return checked;
+  AttnLaunch l;
+  const pa_status built = build_launch(&l, plan, out, query, key_cache, value_cache, kv_dtype, k_scale, v_scale,
+                                       block_tables, max_blocks_per_seq, context_lens, num_seqs, num_heads,
+                                       num_kv_heads, head_size, block_size, num_blocks, scale, workspace);
+  if (built != PA_OK) return built;
+  l.a.q_start = q_start;
+  l.a.num_q_tokens = num_q_tokens;
+  const bool fp8 = is_fp8(kv_dtype);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = q_dtype == PA_BF16
+                            ? pa::launch_rows_bf16(l.tk, l.tv, l.a, fp8, head_size, plan.g_tile, l.grid, st)
+                            : pa::launch_rows_f16(l.tk, l.tv, l.a, fp8, head_size, plan.g_tile, l.grid, st);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace pa_host
@@ -332,10 +384,11 @@ pa_status pa_paged_attention(void* out, const void* query, pa_dtype q_dtype, con
 
 size_t pa_paged_attention_accumulate_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size,
                                                     int max_context_len, int partition_size) {
-  const size_t base = pa_paged_attention_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_context_len,
-                                                        partition_size);
+  const int ps = plan_fine_partition(num_seqs, num_heads, num_kv_heads, max_context_len, partition_size);
+  const size_t base =
+      ps <= 0 ? 0
+              : pa_paged_attention_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_context_len, ps);
   if (base == 0) return 0;
-  const int ps = plan_partition(num_seqs, num_heads, num_kv_heads, max_context_len, partition_size);
   return accumulate_layout(base, num_seqs, num_heads, max_context_len, std::max(1, ceil_div(max_context_len, ps))).total;
 }
 
@@ -348,10 +401,13 @@ pa_status pa_paged_attention_accumulate(void* out, float* scores, int score_stri
                                         float scale, int partition_size, void* workspace, size_t workspace_bytes,
                                         pa_stream_t stream) {
   AttnPlan plan;
+  const int ps = partition_size != 0
+                     ? partition_size
+                     : std::max(0, plan_fine_partition(num_seqs, num_heads, num_kv_heads, max_context_len, 0));
   const pa_status checked = check_attention(out, query, q_dtype, key_cache, value_cache, kv_dtype, k_scale, v_scale,
                                             block_tables, max_blocks_per_seq, context_lens, num_seqs, num_heads,
                                             num_kv_heads, head_size, block_size, num_blocks, max_context_len, scale,
-                                            partition_size, &plan);
+                                            ps, &plan);
   if (checked != PA_OK) return checked;
   if (score_stride <= 0 || score_stride < max_context_len) return PA_ERR_INVALID_ARGUMENT;
   if (plan.empty) return PA_OK;

@@ -78,6 +78,10 @@ constexpr int kMsgBlkShift = 4;  // StageMsg.flags: bits 0-3 flags, bits 4-31 bo
 constexpr int kMsgLast = 2;
 constexpr int kMsgBadBlock = 4;
 
+// What a launch of paged_attention_main computes. kDecode: row s of query and out belongs to sequence s.
+// kDecodeWeights: the same, and what the attention weights are formed from. kDecodeRows: rows by q_start.
+enum DecodeMode { kDecode = 0, kDecodeWeights = 1, kDecodeRows = 2 };
+
 struct AttnArgs {
   void* out;                    // [S][H][D] query dtype
   const void* query;            // [S][H][D]
@@ -108,6 +112,9 @@ struct AttnArgs {
   float* logits;
   float2* stats;                // [S][H][P]
   long long logit_stride;
+  // Query rows by chunk (kDecodeRows only): sequence s has row q_start[s] of num_q_tokens, or none.
+  const int32_t* q_start;       // [S + 1]
+  int num_q_tokens;
   unsigned long long* trace;    // timing records, written only by builds with PA_TRACE defined (else null)
 };
 
@@ -167,8 +174,17 @@ struct StageMsg {
   int blk1;    // physical blocks of the stage's two 8-token boxes, for per-block scales (0 when a box
 };             // is not loaded); box 0's is carried in flags >> kMsgBlkShift
 
+// The query row of sequence s (kDecodeRows): q_start[s], kRowNone without new tokens, kRowInvalid when the chunk
+// does not lie in the query array.
+constexpr int kRowNone = -1, kRowInvalid = -2;
+__device__ __forceinline__ int query_row(int s, const AttnArgs& a) {
+  const int row = __ldg(a.q_start + s), n = __ldg(a.q_start + s + 1) - row;
+  if (n == 0) return kRowNone;
+  return n < 0 || row < 0 || row > a.num_q_tokens - n ? kRowInvalid : row;
+}
+
 struct ItemInfo {
-  int s, part, kvh0, h_sub, heads, write_final, pad0, pad1;  // h_sub: first query-head offset in a group
+  int s, part, kvh0, h_sub, heads, write_final, pad0, qrow;  // h_sub: first query-head offset in a group; qrow: row of query and out
 };
 
 // Work order of one launch, built by every CTA from the context lengths (the same table in each):
@@ -416,16 +432,18 @@ __device__ __forceinline__ ItemCoord decode_ordered(unsigned int t, const AttnAr
 
 // BS: FP8 cache with per-(block, kv head) scales (args.scale_block_stride != 0); a separate
 // instantiation so that the per-head FP8 path carries none of its work.
-// W: also writes every token's scaled score and each item's softmax statistics, from which
+// kDecodeWeights (W): also writes every token's scaled score and each item's softmax statistics, from which
 // attention_weights_kernel (pa_weights.cuh) forms the normalised weights. Kept apart from the plain
 // instantiations, whose code and results it leaves as they are. The sum of a W item's statistics takes
 // the weights before their rounding to 16 bits (l_run takes the rounded ones that enter P V): scores
 // accumulate over thousands of steps and carry fp32 accuracy.
-template <typename QT, typename KVT, int D, int G, bool BS, bool W = false>
+// kDecodeRows (R): sequences without a query row are skipped.
+template <typename QT, typename KVT, int D, int G, bool BS, int MODE = kDecode>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                      const AttnArgs args) {
   constexpr int EB = Elem<KVT>::kBytes;
+  constexpr bool W = MODE == kDecodeWeights, R = MODE == kDecodeRows;
   using S = Shape<D, G, EB>;
   using Lay = Layout<QT, D, G, EB>;
   using Piece = typename Elem<KVT>::Piece;
@@ -500,6 +518,7 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
     unsigned int cur_idx = 0, nxt_idx = 0;
     ItemCoord cur_c{}, nxt_c{};
     int cur_L = 0, nxt_L = 0;
+    int cur_row = 0, nxt_row = 0;  // R: query row, negative when there is none
     int cur_ids[kIdWindow], nxt_ids[kIdWindow];
     bool have_next = false;
 #define PA_PREPARE(IDX, C, LV, IDS)                                                                    \
@@ -507,6 +526,7 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
     if ((IDX) < num_tickets) {                                                                         \
       C = ordered ? decode_ordered((IDX), args, order) : decode_item((IDX), args);                     \
       LV = __ldg(args.context_lens + C.s);                                                             \
+      if constexpr (R) cur_row = query_row(C.s, args);                                                 \
       if (C.part < 0) C.part = (LV > 0 && !context_len_invalid(LV, args)) ? (LV - 1) / args.partition_size : 0; \
       const int need_ = LV <= 0 ? 0 : cmin(args.max_blocks_per_seq, LV / bs + (LV % bs != 0));         \
       const int32_t* row_ = args.block_tables + static_cast<size_t>(C.s) * args.max_blocks_per_seq;    \
@@ -528,6 +548,7 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
       if (nxt_idx < num_tickets) {                                                                     \
         nxt_c = ordered ? decode_ordered(nxt_idx, args, order) : decode_item(nxt_idx, args);           \
         nxt_L = __ldg(args.context_lens + nxt_c.s);                                                    \
+        if constexpr (R) nxt_row = query_row(nxt_c.s, args);                                           \
       }                                                                                                \
     } else if (claim_step == 2) {                                                                      \
       if (nxt_idx < num_tickets) {                                                                     \
@@ -564,7 +585,11 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
       const int kv_here = cmin(kHeadBlock, args.num_kv_heads - kvh0);
       const int h_sub = c.sub * G;                       // first query head of the subgroup in a group
       const int heads = cmin(G, args.group - h_sub);     // query heads per kv head in this item
-      if (c.part < cmax(n_parts, 1)) {
+      if constexpr (R) {
+        if (cur_row == kRowInvalid && lane == 0) atomicOr(err, PA_DEVERR_CONTEXT_LEN);
+      }
+      const int qrow = R ? cur_row : c.s;
+      if (c.part < cmax(n_parts, 1) && (!R || qrow >= 0)) {
         if (L == 0 || bad_len) {
           // Empty context -> zeros; a context the launch cannot cover -> NaN and an error bit.
           if (bad_len && lane == 0) atomicOr(err, PA_DEVERR_CONTEXT_LEN);
@@ -572,7 +597,7 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
           for (int i = lane; i < kv_here * heads * D; i += 32) {
             const int kv = i / (heads * D), g = (i / D) % heads, e = i % D;
             const size_t h = static_cast<size_t>(kvh0 + kv) * args.group + h_sub + g;
-            static_cast<QT*>(args.out)[(static_cast<size_t>(c.s) * args.num_heads + h) * D + e] = QT(fill);
+            static_cast<QT*>(args.out)[(static_cast<size_t>(qrow) * args.num_heads + h) * D + e] = QT(fill);
           }
         } else {
           const int tok_begin = c.part * args.partition_size;
@@ -596,7 +621,7 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
             inf.heads = heads;
             inf.write_final = n_parts <= 1;
             inf.pad0 = static_cast<int>(cur_idx);
-            inf.pad1 = 0;
+            inf.qrow = qrow;
 #ifdef PA_TRACE
             unsigned long long* rec = args.trace + kTraceItemBase + 4ull * cur_idx;
             rec[0] = global_timer_ns();
@@ -611,7 +636,7 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
           for (int r = lane; r < kv_here * heads; r += 32) {
             const int kv = r / heads, g = r - kv * heads;
             const QT* qsrc = static_cast<const QT*>(args.query) +
-                             (static_cast<size_t>(c.s) * args.num_heads + (kvh0 + kv) * args.group + h_sub + g) * D;
+                             (static_cast<size_t>(qrow) * args.num_heads + (kvh0 + kv) * args.group + h_sub + g) * D;
             bulk_copy_g2s(smem + Lay::kQuery + qb * Lay::kQueryOne + (kv * G + g) * Lay::kQRow * sizeof(QT), qsrc,
                           static_cast<uint32_t>(D * sizeof(QT)), &qfull[qb]);
           }
@@ -684,6 +709,7 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
       cur_idx = nxt_idx;
       cur_c = nxt_c;
       cur_L = nxt_L;
+      if constexpr (R) cur_row = nxt_row;
 #pragma unroll
       for (int j = 0; j < kIdWindow; ++j) cur_ids[j] = nxt_ids[j];
     }
@@ -1113,7 +1139,7 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
             if (t4 == 0) args.stats[rowi] = make_float2(m_run, poisoned ? __int_as_float(0x7fc00000) : le);
           }
           if (inf.write_final) {
-            QT* out = static_cast<QT*>(args.out) + (static_cast<size_t>(inf.s) * args.num_heads + h) * D;
+            QT* out = static_cast<QT*>(args.out) + (static_cast<size_t>(R ? inf.qrow : inf.s) * args.num_heads + h) * D;
             if constexpr (EB == 2) {
 #pragma unroll
               for (int nb = 0; nb < S::kNBlocks; ++nb)
@@ -1176,7 +1202,8 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
                     make_float2(mg, poisoned ? __int_as_float(0x7fc00000) : lg);
             }
             if (inf.write_final) {
-              QT* out = static_cast<QT*>(args.out) + (static_cast<size_t>(inf.s) * args.num_heads + h) * D + dp * 8;
+              QT* out = static_cast<QT*>(args.out) +
+                        (static_cast<size_t>(R ? inf.qrow : inf.s) * args.num_heads + h) * D + dp * 8;
               *reinterpret_cast<uint2*>(out) = pack4<QT>(acc[g][0].x * r, acc[g][0].y * r, acc[g][1].x * r, acc[g][1].y * r);
               *reinterpret_cast<uint2*>(out + 4) = pack4<QT>(acc[g][2].x * r, acc[g][2].y * r, acc[g][3].x * r, acc[g][3].y * r);
             } else {
@@ -1252,7 +1279,8 @@ __device__ __forceinline__ void merge_range(const AttnArgs& a, size_t base, int 
 // were finished by the main kernel.
 // MAXP (SPLIT = false): a bound on the partition count the launch was sized for (4, 8 or 16), so that a
 // row's preloaded values take no more registers than it needs and more warps stay resident.
-template <typename QT, int D, bool SPLIT, int MAXP = kReduceSplitAbove>
+// ROWS: the row of out is found through q_start (kDecodeRows).
+template <typename QT, int D, bool SPLIT, int MAXP = kReduceSplitAbove, bool ROWS = false>
 __global__ void __launch_bounds__(kReduceWarps * 32)
 paged_attention_reduce(const AttnArgs args) {
   constexpr int kPer = D / 32;  // elements per lane: 4 for d = 128, 2 for d = 64
@@ -1276,6 +1304,12 @@ paged_attention_reduce(const AttnArgs args) {
   if (L <= 0 || context_len_invalid(L, args)) return;
   const int n_parts = (L + PS - 1) / PS;
   if (n_parts <= 1) return;
+  long out_row = row;
+  if constexpr (ROWS) {
+    const int q = query_row(s, args);
+    if (q < 0) return;
+    out_row = static_cast<long>(q) * args.num_heads + row % args.num_heads;
+  }
   const size_t base = static_cast<size_t>(row) * args.num_partitions;
   float wsum = 0.f;
   float acc[kPer];
@@ -1390,7 +1424,7 @@ paged_attention_reduce(const AttnArgs args) {
     }
   }
   const float r = 1.0f / wsum;
-  QT* out = static_cast<QT*>(args.out) + static_cast<size_t>(row) * D + lane * kPer;
+  QT* out = static_cast<QT*>(args.out) + static_cast<size_t>(out_row) * D + lane * kPer;
   if constexpr (kPer == 4) {
     *reinterpret_cast<uint2*>(out) = pack4<QT>(acc[0] * r, acc[1] * r, acc[2] * r, acc[3] * r);
   } else {

@@ -50,7 +50,11 @@ size_t pa_paged_cross_attention_workspace_size(int num_seqs, int num_q_tokens, i
   if (num_seqs < 0 || num_q_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
       head_size <= 0 || max_q_len < 0 || max_context_len < 0)
     return 0;
-  return plan_cross(num_seqs, num_q_tokens, num_heads, num_kv_heads, head_size, max_q_len, max_context_len).total;
+  const size_t tiles =
+      plan_cross(num_seqs, num_q_tokens, num_heads, num_kv_heads, head_size, max_q_len, max_context_len).total;
+  if (max_q_len > 1) return tiles;
+  return std::max(tiles,
+                  pa_host::decode_rows_workspace(num_seqs, num_heads, num_kv_heads, head_size, max_context_len));
 }
 
 pa_status pa_paged_cross_attention(void* out, const void* query, pa_dtype q_dtype, const void* key_cache,
@@ -69,6 +73,14 @@ pa_status pa_paged_cross_attention(void* out, const void* query, pa_dtype q_dtyp
       context_lens, q_start, num_seqs, num_q_tokens, num_heads, num_kv_heads, head_size, block_size, num_blocks,
       max_q_len, scale, workspace, workspace_bytes, need, &empty);
   if (checked != PA_OK || empty) return checked;
+  // Single tokens are bound by the states' bytes: the decode kernel reads them at 90% of the copy bandwidth, a
+  // tile of 128 query rows with few of them used at half (32 sequences, 8 kv heads, up to 6404 states:
+  // TIMES).
+  if (max_q_len == 1 && pa_host::decode_rows_supported(block_size, num_blocks))
+    return pa_host::decode_rows(out, query, q_dtype, key_cache, value_cache, kv_dtype, k_scale, v_scale, block_tables,
+                                max_blocks_per_seq, context_lens, q_start, num_seqs, num_q_tokens, num_heads,
+                                num_kv_heads, head_size, block_size, num_blocks, max_context_len, scale, workspace,
+                                stream);
   pa_host::PrefillLaunch l;
   const pa_status built = pa_host::build_prefill(
       &l, out, query, key_cache, value_cache, kv_dtype, k_scale, v_scale, block_tables, max_blocks_per_seq,

@@ -130,6 +130,26 @@ __device__ __forceinline__ void named_barrier(uint32_t id, uint32_t count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
+// Barrier over every thread of the cluster; memory accesses before it are performed before those after it.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The same without the ordering of memory accesses.
+__device__ __forceinline__ void cluster_barrier_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// The word at this address in the shared memory of the cluster's CTA `rank`.
+template <typename T>
+__device__ __forceinline__ T cluster_load(const T* p, int rank) {
+  static_assert(sizeof(T) == 4, "one word");
+  uint32_t addr, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return static_cast<T>(v);
+}
+
 // ------------------------------------------------------------------------------------------------
 // Packed conversions to float2 (8 elements = one 16-byte or 8-byte piece of a row).
 // ------------------------------------------------------------------------------------------------

@@ -1,5 +1,5 @@
 // pa_evict.cu -- C ABI of the eviction by accumulated attention weight (include/pagedattn.h): validation
-// before any CUDA call, then the selection and the move (pa_evict.cuh).
+// before any CUDA call, then pa::evict_kernel (pa_evict.cuh).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -38,8 +38,8 @@ extern "C" pa_status pa_evict_tokens(int32_t* kept, int32_t* new_lens, float* sc
   // A token that moves to another block would need its codes scaled anew.
   if (kv_dtype == PA_FP8_E4M3_BLOCK) return PA_ERR_UNSUPPORTED;
   const int64_t row_bytes = static_cast<int64_t>(head_size) * pa_host::elem_bytes(kv_dtype);
-  if (row_bytes % 16 != 0 || row_bytes > 1024 || num_seqs > 65535 || score_stride > (1 << 30) ||
-      budget > (1 << 30))
+  if (row_bytes % 16 != 0 || row_bytes > 1024 || num_seqs > 65535 || num_kv_heads > 65535 || score_stride > (1 << 30) ||
+      budget > (1 << 30) || static_cast<int64_t>(num_blocks) * block_size >= pa::kNoMove)
     return PA_ERR_UNSUPPORTED;
 
   pa::EvictArgs a{};
@@ -64,13 +64,25 @@ extern "C" pa_status pa_evict_tokens(int32_t* kept, int32_t* new_lens, float* sc
   a.budget = budget;
   a.num_sink = num_sink;
   a.num_recent = num_recent;
+  a.log_block = -1;
+  for (int i = 0; i < 31; ++i)
+    if (block_size == 1 << i) a.log_block = i;
+  // A row's strip is as wide as the row up to 256 bytes: whole 128-byte lines a request.
+  a.log_lanes = pa::kMoveMinLogLanes;
+  while (a.log_lanes < 4 && (16 << a.log_lanes) < row_bytes) ++a.log_lanes;
+  int device = 0, sms = 0;
+  if (cudaGetDevice(&device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || sms <= 0)
+    return PA_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const unsigned heads = static_cast<unsigned>(num_kv_heads), seqs = static_cast<unsigned>(num_seqs);
-  cudaError_t e = pa_host::launch_overlapped(pa::evict_select_kernel, dim3(heads, seqs), dim3(pa::kSelectThreads), 0,
-                                             st, a);
-  if (e != cudaSuccess) return PA_ERR_CUDA;
-  const unsigned strips = static_cast<unsigned>((row_bytes + 63) / 64);
-  e = pa_host::launch_overlapped(pa::evict_move_kernel, dim3(heads, seqs, (2 * strips + pa::kMoveWarps - 1) / pa::kMoveWarps),
-                                 dim3(pa::kMoveWarps * 32), 0, st, a);
+  // As many CTAs a row as the GPU holds at once, so that no row waits for another's CTAs (16 rows of 16384 tokens
+  // x 8 heads, cut to 2048: 4 CTAs 69 us, 2 CTAs 90 us, 8 CTAs, two waves, 83 us), but none without a share.
+  const int64_t fit = static_cast<int64_t>(sms) * pa::kEvictPerSm / (static_cast<int64_t>(heads) * seqs);
+  const int64_t share = pa_host::ceil_div(max_context_len, pa::kEvictShare);
+  const unsigned cluster = static_cast<unsigned>(
+      std::max<int64_t>(1, std::min<int64_t>(pa::kEvictCluster, std::min(fit, share))));
+  const cudaError_t e = pa_host::launch_overlapped_clusters(cluster, pa::evict_kernel, dim3(cluster, heads, seqs),
+                                                            dim3(pa::kEvictThreads), 0, st, a);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

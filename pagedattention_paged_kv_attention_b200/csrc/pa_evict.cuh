@@ -6,11 +6,16 @@
 // token kept[j] becomes token j, in the destination table's blocks. Each head keeps tokens of its own;
 // attention does not depend on which slot a key sits in, so heads need only agree on their number.
 //
-// evict_select_kernel finds the kept tokens: a radix selection of the q-th largest score on a monotone
-// 32-bit image of the fp32 values, three digits of 11, 11 and 10 bits, then one ordered compaction.
-// evict_move_kernel moves the rows. A kept token never moves up (kept[j] >= j), so a warp that walks j
-// upwards, reading a group of rows before it writes them, may write over the very blocks it reads:
-// a slot it writes is a source only of rows it has read already.
+// One cluster of CTAs per (sequence, kv head) does both steps, so that one cluster's selection runs while
+// another's rows move, and the scores cross the chip once.
+// Selection: a radix selection of the q-th largest score on a monotone 32-bit image of the fp32 values, up
+// to four digits of 8 bits (few candidates left after a digit are ranked directly, usually after the second),
+// then one ordered compaction. The keys of up to kEvictPer tokens a thread stay in registers. A digit is
+// counted in 16 copies of the histogram, one per two lanes, since scores crowd into few exponents and one copy
+// would serialise a warp's atomics; the CTAs' counts are added through distributed shared memory.
+// Move: bound by HBM, every kept row is read and written once. A kept token never moves up (kept[j] >= j), so
+// walking j upwards, a round of rows read before any of them is written, may write over the very blocks that
+// are read: a slot is written after the rows that come from it were read.
 #pragma once
 
 #include <math.h>
@@ -19,11 +24,21 @@
 
 namespace pa {
 
-constexpr int kSelectThreads = 1024;
-constexpr int kSelectBins = 2048;
-constexpr int kMoveWarps = 8;
-constexpr int kMoveRows = 8;          // rows of a warp's load: 4 lanes x 16 bytes each
-constexpr int kMoveUnroll = 8;        // loads in flight per lane
+constexpr int kEvictThreads = 256;
+constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kEvictPerSm = 4;        // CTAs that an SM holds
+constexpr int kEvictCluster = 8;      // most CTAs of a cluster
+constexpr int kEvictShare = 1024;     // fewest tokens worth a CTA of their own
+constexpr int kEvictPer = 16;         // tokens of a tile per thread
+constexpr int kEvictTile = kEvictPer * kEvictThreads;
+constexpr int kHistCopies = 16;
+constexpr int kEvictFew = 32;         // keys that are ranked among themselves
+constexpr int kMoveUnroll = 4;        // 16-byte loads per lane and step; two steps are in flight
+constexpr int kMoveLogLoads = 5;      // log2 of a CTA's warps x loads
+static_assert(kEvictWarps * kMoveUnroll == 1 << kMoveLogLoads, "a round is a power of two");
+constexpr int kMoveMinLogLanes = 2;
+constexpr int kMoveStage = 2048;      // rows of a CTA whose slots are resolved at a time, whole rounds of them
+constexpr uint32_t kNoMove = 0xffffffffu;
 
 struct EvictArgs {
   int32_t* kept;                // [S][Hkv][budget]
@@ -37,7 +52,8 @@ struct EvictArgs {
   const int32_t* context_lens;  // [S]
   unsigned int* error_word;
   int score_stride, max_blocks_per_seq, max_dst_blocks_per_seq, num_kv_heads, row_bytes, block_size, num_blocks,
-      max_context_len, budget, num_sink, num_recent;
+      max_context_len, budget, num_sink, num_recent, log_lanes,
+      log_block;  // log2(block_size), or -1
 };
 
 __device__ __forceinline__ bool evict_len_invalid(int L, const EvictArgs& a) {
@@ -52,170 +68,387 @@ __device__ __forceinline__ uint32_t score_key(float w) {
   return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 
-// One CTA per (kv head, sequence).
-__global__ void __launch_bounds__(kSelectThreads)
-evict_select_kernel(const EvictArgs a) {
-  __shared__ int hist[kSelectBins];
-  __shared__ int warp_gt[kSelectThreads / 32], warp_eq[kSelectThreads / 32];
-  __shared__ uint32_t sh_prefix;
-  __shared__ int sh_need;
+// Place of key i of a tile in shared memory: each thread's kEvictPer consecutive keys, 16 bytes apart from the
+// next thread's, so that 16-byte reads of a warp do not meet in a bank.
+__device__ __forceinline__ int key_slot(int i) { return i + i / kEvictPer * 4; }
+
+struct EvictShared {
+  union {
+    struct {
+      int hist[256 * kHistCopies];                // [digit][lane % kHistCopies]
+      uint32_t keys[kEvictTile / kEvictPer * (kEvictPer + 4)];
+    };
+    struct {
+      uint32_t slots[2 * kMoveStage];             // of a stage's rows: from (kNoMove: the row stays), then to
+      float score[kMoveStage];
+    };
+  };
+  int bins[2][256];                    // read by the cluster's other CTAs, as the next three
+  uint32_t few[kEvictFew];
+  int num_few, cta_sum[2];
+  uint32_t all_few[kEvictFew];
+  int warp_sum[kEvictWarps][2];
+  uint32_t prefix;
+  int need, count;
+};
+
+// Keys of tokens that are not ranked: past the row, or kept whatever their score.
+constexpr uint32_t kKeyOut = 0u, kKeyEnd = 0xffffffffu;  // no score's key is either
+
+__device__ __forceinline__ void evict_sync(int ctas) {
+  if (ctas > 1)
+    cluster_barrier();
+  else
+    __syncthreads();
+}
+
+// Exclusive scan of (x, y) over the CTA's threads, 0 <= x, y <= kEvictPer; *total receives the sums.
+__device__ __forceinline__ int2 evict_scan(EvictShared& sh, int x, int y, int2* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int v = x | (y << 16);               // at most kEvictTile = 2^12 each
+  const int own = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();                     // the last scan's sums have been read
+  if (lane == 31) sh.warp_sum[warp][0] = v;
+  __syncthreads();
+  int all = 0, before = v - own;
+#pragma unroll
+  for (int i = 0; i < kEvictWarps; ++i) {
+    const int c = sh.warp_sum[i][0];
+    before += i < warp ? c : 0;
+    all += c;
+  }
+  *total = make_int2(all & 0xffff, all >> 16);
+  return make_int2(before & 0xffff, before >> 16);
+}
+
+// Selects among L > budget tokens and writes kept. The cluster's CTAs take contiguous chunks, a chunk goes in
+// tiles of kEvictTile tokens, and a thread takes kEvictPer consecutive tokens of a tile.
+__device__ __forceinline__ void evict_select(EvictShared& sh, const EvictArgs& a, int L, int rank, int ctas,
+                                             const float* w, int32_t* kept) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int chunk = (L + ctas - 1) / ctas;
+  const int t0 = min(L, rank * chunk), t1 = min(L, t0 + chunk);
+  const int c0 = a.num_sink, c1 = L - a.num_recent;  // candidates; more than are needed, as L > budget
+  int need = a.budget - a.num_sink - a.num_recent;
+  uint32_t k[kEvictPer];
+  auto load_tile = [&](int tile) {     // read in lines, handed out by threads
+    __syncthreads();
+    uint32_t v[kEvictPer];
+#pragma unroll
+    for (int i = 0; i < kEvictPer; ++i) {
+      const int t = tile + i * kEvictThreads + tid;
+      v[i] = t < t1 ? __float_as_uint(w[t]) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < kEvictPer; ++i) {
+      const int t = tile + i * kEvictThreads + tid;
+      sh.keys[key_slot(i * kEvictThreads + tid)] =
+          t >= t1 ? kKeyOut : t < c0 || t >= c1 ? kKeyEnd : score_key(__uint_as_float(v[i]));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEvictPer; i += 4) {
+      const uint4 q = *reinterpret_cast<const uint4*>(&sh.keys[key_slot(tid * kEvictPer) + i]);
+      k[i] = q.x;
+      k[i + 1] = q.y;
+      k[i + 2] = q.z;
+      k[i + 3] = q.w;
+    }
+  };
+  const bool one_tile = t1 - t0 <= kEvictTile;
+  if (one_tile) load_tile(t0);
+  // f() with each tile's keys in k; the keys of a single tile stay there.
+  auto each_tile = [&](auto f) {
+    if (one_tile) {
+      f(t0);
+    } else {
+      for (int tile = t0; tile < t1; tile += kEvictTile) {
+        load_tile(tile);
+        f(tile);
+      }
+    }
+  };
+  auto ranked = [](uint32_t key) { return key - 1u < kKeyEnd - 1u; };
+  uint32_t threshold = kKeyEnd;        // the need-th largest key; `need` of its equals stay
+  if (need > 0) {
+    uint32_t prefix = 0;
+    for (int i = tid; i < 256 * kHistCopies; i += kEvictThreads) sh.hist[i] = 0;
+    if (tid == 0) sh.num_few = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      each_tile([&](int) {
+#pragma unroll
+        for (int i = 0; i < kEvictPer; ++i)
+          if (ranked(k[i]) && (shift == 24 || (k[i] >> (shift + 8)) == prefix))
+            atomicAdd(&sh.hist[((k[i] >> shift) & 255u) * kHistCopies + lane % kHistCopies], 1);
+      });
+      __syncthreads();
+      // Thread i adds up digit 255 - i, here and then over the cluster; a scan finds the digit, from the top,
+      // at which the count reaches `need`.
+      const int digit = 255 - tid;
+      int* bins = sh.bins[(shift >> 3) & 1];
+      int sum = 0;
+#pragma unroll 8
+      for (int i = 0; i < kHistCopies; ++i) {
+        int* c = &sh.hist[digit * kHistCopies + (i + tid / 2) % kHistCopies];
+        sum += *c;
+        *c = 0;
+      }
+      if (ctas > 1) {
+        bins[digit] = sum;
+        cluster_barrier();
+        sum = 0;
+        for (int r = 0; r < ctas; ++r) sum += cluster_load(&bins[digit], r);
+      }
+      int incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) sh.warp_sum[warp][0] = incl;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kEvictWarps; ++i) incl += i < warp ? sh.warp_sum[i][0] : 0;
+      if (incl - sum < need && incl >= need) {
+        sh.prefix = (prefix << 8) | static_cast<uint32_t>(digit);
+        sh.need = need - (incl - sum);
+        sh.count = sum;
+      }
+      __syncthreads();
+      prefix = sh.prefix;
+      need = sh.need;
+      const int m = sh.count;
+      if (shift == 0) {
+        threshold = prefix;
+      } else if (m <= kEvictFew) {
+        // Few keys share the digits so far: collect them and rank each among them.
+        each_tile([&](int) {
+#pragma unroll
+          for (int i = 0; i < kEvictPer; ++i)
+            if (ranked(k[i]) && (k[i] >> shift) == prefix) sh.few[atomicAdd(&sh.num_few, 1)] = k[i];
+        });
+        evict_sync(ctas);
+        for (int r = 0, at = 0; r < ctas; ++r) {
+          const int c = cluster_load(&sh.num_few, r);
+          if (tid < c) sh.all_few[at + tid] = cluster_load(&sh.few[tid], r);
+          at += c;
+        }
+        __syncthreads();
+        for (int c = warp; c < m; c += kEvictWarps) {
+          const uint32_t mine = sh.all_few[c];
+          int above = 0, equal = 0;
+          for (int i = lane; i < m; i += 32) {
+            above += sh.all_few[i] > mine;
+            equal += sh.all_few[i] == mine;
+          }
+          above = __reduce_add_sync(0xffffffffu, above);
+          equal = __reduce_add_sync(0xffffffffu, equal);
+          if (lane == 0 && above < need && need <= above + equal) {  // every equal of the threshold writes the same
+            sh.prefix = mine;
+            sh.need = need - above;
+          }
+        }
+        __syncthreads();
+        threshold = sh.prefix;
+        need = sh.need;
+        break;
+      }
+    }
+  }
+  // Kept: keys above the threshold (the ends' among them) and the first `need` equal to it.
+  const bool any = threshold != kKeyEnd;
+  const uint32_t above = any ? threshold : kKeyEnd - 1u;
+  int x = 0, y = 0;
+  auto count = [&] {
+    x = y = 0;
+#pragma unroll
+    for (int i = 0; i < kEvictPer; ++i) {
+      x += k[i] > above;
+      y += any && k[i] == threshold;
+    }
+  };
+  int2 carry = make_int2(0, 0), total, at = make_int2(0, 0);
+  if (one_tile || ctas > 1) {
+    each_tile([&](int) {
+      count();
+      at = evict_scan(sh, x, y, &total);
+      carry.x += total.x;
+      carry.y += total.y;
+    });
+  }
+  if (ctas > 1) {
+    if (tid == 0) {
+      sh.cta_sum[0] = carry.x;
+      sh.cta_sum[1] = carry.y;
+    }
+    cluster_barrier();
+  }
+  carry = make_int2(0, 0);
+  for (int r = 0; r < rank; ++r) {
+    carry.x += cluster_load(&sh.cta_sum[0], r);
+    carry.y += cluster_load(&sh.cta_sum[1], r);
+  }
+  each_tile([&](int tile) {
+    if (!one_tile) {
+      count();
+      at = evict_scan(sh, x, y, &total);
+    }
+    int eq = carry.y + at.y, place = carry.x + at.x + min(eq, need);
+    const int t = tile + tid * kEvictPer;
+#pragma unroll
+    for (int i = 0; i < kEvictPer; ++i) {
+      const bool is_eq = any && k[i] == threshold;
+      if (k[i] > above || (is_eq && eq < need)) kept[place++] = t + i;
+      eq += is_eq;
+    }
+    if (!one_tile) {
+      carry.x += total.x;
+      carry.y += total.y;
+    }
+  });
+}
+
+// grid (cluster, kv heads, sequences). In the move a strip is 16 << log_lanes bytes of the head's key or value
+// row, and a step is one strip of a round, kMoveUnroll loads of 32 >> log_lanes rows a warp and CTA. The cluster's
+// barrier parts a step's reads from its writes; the next step's rows are loaded before it (a slot is never
+// written before its row has been read, so reading early is safe). The scores move with the rows.
+__global__ void __launch_bounds__(kEvictThreads, kEvictPerSm)
+evict_kernel(const EvictArgs a) {
+  __shared__ EvictShared sh;
   grid_dependency_wait();
   grid_dependents_launch();
-  const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x, ctas = gridDim.x, h = blockIdx.y, s = blockIdx.z;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const size_t rowi = static_cast<size_t>(s) * a.num_kv_heads + h;
   int32_t* kept = a.kept + rowi * a.budget;
-  const float* w = a.scores + rowi * a.score_stride;
-  float* wo = a.scores_out + rowi * a.score_stride;
   const int L = a.context_lens[s];
-  if (evict_len_invalid(L, a)) {
-    if (tid == 0) {
+  if (evict_len_invalid(L, a)) {  // the whole cluster alike
+    if (tid == 0 && rank == 0) {
       atomicOr(a.error_word, PA_DEVERR_CONTEXT_LEN);
       if (h == 0) a.new_lens[s] = 0;
     }
-    for (int j = tid; j < a.budget; j += kSelectThreads) kept[j] = -1;
+    for (int j = rank * kEvictThreads + tid; j < a.budget; j += ctas * kEvictThreads) kept[j] = -1;
     return;
   }
+  const float* w = a.scores + rowi * a.score_stride;
+  float* wo = a.scores_out + rowi * a.score_stride;
   const int n = min(L, a.budget);
-  if (h == 0 && tid == 0) a.new_lens[s] = n;
-  for (int j = n + tid; j < a.budget; j += kSelectThreads) kept[j] = -1;
   if (L <= a.budget) {
-    for (int j = tid; j < n; j += kSelectThreads) kept[j] = j;
+    for (int j = rank * kEvictThreads + tid; j < n; j += ctas * kEvictThreads) kept[j] = j;
   } else {
-    const int c0 = a.num_sink, c1 = L - a.num_recent;  // candidates; c1 - c0 > need as L > budget
-    int need = a.budget - a.num_sink - a.num_recent;
-    uint32_t prefix = 0;                               // leading digits of the need-th largest key
-    int shift = 32;
-    if (need > 0) {
-#pragma unroll 1
-      for (int pass = 0; pass < 3; ++pass) {
-        const int bits = pass < 2 ? 11 : 10, high = shift;
-        shift -= bits;
-        for (int i = tid; i < kSelectBins; i += kSelectThreads) hist[i] = 0;
-        __syncthreads();
-        for (int t = c0 + tid; t < c1; t += kSelectThreads) {
-          const uint32_t k = score_key(w[t]);
-          if (pass == 0 || (k >> high) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1);
-        }
-        __syncthreads();
-        if (warp == 0) {  // the digit whose suffix count reaches `need`
-          const int per = (1 << bits) / 32, top = (1 << bits) - 1;
-          int sum = 0;
-          for (int i = 0; i < per; ++i) sum += hist[top - (lane * per + i)];
-          int incl = sum;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-          }
-          int run = incl - sum;
-          if (run < need && incl >= need) {
-            int i = 0;
-            while (run + hist[top - (lane * per + i)] < need) run += hist[top - (lane * per + i++)];
-            sh_prefix = (prefix << bits) | static_cast<uint32_t>(top - (lane * per + i));
-            sh_need = need - run;
-          }
-        }
-        __syncthreads();
-        prefix = sh_prefix;
-        need = sh_need;
-      }
-    }
-    // Kept: the ends, keys above the threshold `prefix`, and the first `need` equal to it (need == 0: no
-    // candidate at all). Each warp takes a contiguous segment; counts first, then places.
-    const bool any = a.budget > a.num_sink + a.num_recent;
-    const int seg = (L + kSelectThreads - 1) / kSelectThreads * 32;
-    const int t0 = min(L, warp * seg), t1 = min(L, t0 + seg);
-    int gt = 0, eq = 0;
-    for (int t = t0 + lane; t < t1; t += 32) {
-      const bool end = t < c0 || t >= c1;
-      const uint32_t k = score_key(w[t]);
-      gt += end || (any && k > prefix);
-      eq += !end && any && k == prefix;
-    }
-    gt = __reduce_add_sync(0xffffffffu, gt);
-    eq = __reduce_add_sync(0xffffffffu, eq);
-    if (lane == 0) {
-      warp_gt[warp] = gt;
-      warp_eq[warp] = eq;
-    }
-    __syncthreads();
-    int eq_before = lane < warp ? warp_eq[lane] : 0, gt_before = lane < warp ? warp_gt[lane] : 0;
-    eq_before = __reduce_add_sync(0xffffffffu, eq_before);
-    gt_before = __reduce_add_sync(0xffffffffu, gt_before);
-    int place = gt_before + min(eq_before, need);
-    const unsigned lt = (1u << lane) - 1u;
-    for (int b = t0; b < t1; b += 32) {
-      const int t = b + lane;
-      const bool in = t < t1;
-      const bool end = in && (t < c0 || t >= c1);
-      const uint32_t k = in ? score_key(w[t]) : 0u;
-      const bool is_eq = in && !end && any && k == prefix;
-      const unsigned eqs = __ballot_sync(0xffffffffu, is_eq);
-      const bool take = end || (in && any && k > prefix) || (is_eq && eq_before + __popc(eqs & lt) < need);
-      const unsigned takes = __ballot_sync(0xffffffffu, take);
-      if (take) kept[place + __popc(takes & lt)] = t;
-      place += __popc(takes);
-      eq_before += __popc(eqs);
-    }
+    evict_select(sh, a, L, rank, ctas, w, kept);
   }
-  __syncthreads();
-  // The scores move with their tokens, a group read before it is written (scores_out may be scores); the
-  // rest of the row starts from zero.
-  for (int b = 0; b < n; b += kSelectThreads) {
-    const int j = b + tid;
-    const float x = j < n ? w[kept[j]] : 0.f;
-    __syncthreads();
-    if (j < n) wo[j] = x;
-  }
-  __syncthreads();
-  for (int j = n + tid; j < a.score_stride; j += kSelectThreads) wo[j] = 0.f;
-}
+  evict_sync(ctas);  // kept is complete; nothing reads this CTA's shared memory any more
 
-// grid (kv heads, sequences, groups of kMoveWarps strips); each warp moves one 64-byte strip of the head's key or
-// value rows.
-__global__ void __launch_bounds__(kMoveWarps * 32)
-evict_move_kernel(const EvictArgs a) {
-  grid_dependency_wait();
-  grid_dependents_launch();
-  const int h = blockIdx.x, s = blockIdx.y, lane = threadIdx.x & 31;
-  const int warp = blockIdx.z * kMoveWarps + (threadIdx.x >> 5);
-  const int L = a.context_lens[s];
-  const int strips = (a.row_bytes + 63) / 64;
-  if (evict_len_invalid(L, a) || warp >= 2 * strips) return;
-  const int n = min(L, a.budget);
-  uint8_t* cache = warp < strips ? a.key_cache : a.value_cache;
-  const int col = (warp % strips) * 64 + (lane & 3) * 16;
-  if (col >= a.row_bytes) cache = nullptr;  // ragged last strip: these lanes only keep the warp together
-  const int32_t* kept = a.kept + (static_cast<size_t>(s) * a.num_kv_heads + h) * a.budget;
+  const int strips = (a.row_bytes + (16 << a.log_lanes) - 1) / (16 << a.log_lanes);
+  const int rows = 32 >> a.log_lanes;                        // of one load
+  const int log_round = kMoveLogLoads + 5 - a.log_lanes, round = 1 << log_round;  // rows of this CTA and round
   const int32_t* src = a.block_tables + static_cast<size_t>(s) * a.max_blocks_per_seq;
   const int32_t* dst = a.dst_tables + static_cast<size_t>(s) * a.max_dst_blocks_per_seq;
   const size_t token_bytes = static_cast<size_t>(a.num_kv_heads) * a.row_bytes;
-  const size_t head_off = static_cast<size_t>(h) * a.row_bytes + col;
-  const int bs = a.block_size;
-  for (int base = 0; base < n; base += kMoveRows * kMoveUnroll) {
-    uint4 x[kMoveUnroll];
-    uint8_t* to[kMoveUnroll];
-#pragma unroll
-    for (int i = 0; i < kMoveUnroll; ++i) {
-      const int j = base + i * kMoveRows + (lane >> 2);
-      to[i] = nullptr;
-      if (j < n && cache) {
+  const int bs = a.block_size, log_bs = a.log_block;
+  auto in_block = [&](int t) { return log_bs >= 0 ? t >> log_bs : t / bs; };
+  const int row0 = warp * (kMoveUnroll * rows) + (lane >> a.log_lanes);
+  const int lane_col = (lane & ((1 << a.log_lanes) - 1)) * 16;
+  const int stage_rounds = kMoveStage / round;
+  for (int lo = 0; lo < n; lo += stage_rounds * ctas * round) {
+    // The stage's rounds are dealt over the CTAs in turn: row i of this CTA is token j.
+    const int rounds = min(stage_rounds, (n - lo + ctas * round - 1) / (ctas * round));
+    if (lo > 0) __syncthreads();
+#pragma unroll 4
+    for (int i = tid; i < rounds * round; i += kEvictThreads) {
+      const int j = lo + (((i >> log_round) * ctas + rank) << log_round) + (i & (round - 1));
+      uint32_t f = kNoMove;
+      if (j < n) {
         const int t = kept[j];
-        const int sb = src[t / bs], db = dst[j / bs];
-        if (sb < 0 || sb >= a.num_blocks || db < 0 || db >= a.num_blocks) {
+        sh.score[i] = w[t];
+        const int tb = in_block(t), jb = in_block(j);
+        const int sb = src[tb], db = dst[jb];
+        const uint32_t d = static_cast<uint32_t>(db) * bs + (j - jb * bs);
+        if (sb < 0 || sb >= a.num_blocks || db < 0 || db >= a.num_blocks)
           atomicOr(a.error_word, PA_DEVERR_BLOCK_ID);
-        } else if (sb != db || t % bs != j % bs) {
-          const uint8_t* from = cache + (static_cast<size_t>(sb) * bs + t % bs) * token_bytes + head_off;
-          to[i] = cache + (static_cast<size_t>(db) * bs + j % bs) * token_bytes + head_off;
-          x[i] = *reinterpret_cast<const uint4*>(from);
+        else if ((f = static_cast<uint32_t>(sb) * bs + (t - tb * bs)) == d)
+          f = kNoMove;
+        sh.slots[kMoveStage + i] = d;
+      }
+      sh.slots[i] = f;
+    }
+    __syncthreads();
+    // Step = (round, strip); the loads run one step ahead of the stores, each with a cursor of its own.
+    struct Cursor {
+      int round, strip;
+      const uint32_t* from;
+    };
+    auto column = [&](int strip) {  // this lane's column of the strip; null when it has none
+      const bool value = strip >= strips;
+      const int col = ((value ? strip - strips : strip) << (a.log_lanes + 4)) + lane_col;
+      return col < a.row_bytes ? (value ? a.value_cache : a.key_cache) + static_cast<size_t>(h) * a.row_bytes + col : nullptr;
+    };
+    auto next = [&](Cursor& c) {
+      if (++c.strip == 2 * strips) {
+        c.strip = 0;
+        ++c.round;
+        c.from += round;
+      }
+    };
+    auto load = [&](uint4 (&x)[kMoveUnroll], Cursor& c) {
+      if (c.round < rounds) {
+        const uint8_t* base = column(c.strip);
+#pragma unroll
+        for (int i = 0; i < kMoveUnroll; ++i) {
+          const uint32_t f = c.from[rows * i];
+          if (base && f != kNoMove) x[i] = __ldcg(reinterpret_cast<const uint4*>(base + f * token_bytes));
         }
       }
-    }
-    __syncwarp();  // every lane has read its rows before any lane writes
+      next(c);
+    };
+    auto store = [&](const uint4 (&x)[kMoveUnroll], Cursor& c) {
+      uint8_t* base = column(c.strip);
 #pragma unroll
-    for (int i = 0; i < kMoveUnroll; ++i)
-      if (to[i]) *reinterpret_cast<uint4*>(to[i]) = x[i];
+      for (int i = 0; i < kMoveUnroll; ++i) {
+        if (base && c.from[rows * i] != kNoMove)
+          *reinterpret_cast<uint4*>(base + (c.from + kMoveStage)[rows * i] * token_bytes) = x[i];
+      }
+      next(c);
+    };
+    // Waits until this lane's rows of a step have arrived, then for the cluster: the barrier itself orders
+    // no memory (one that does would wait for the stores before it as well).
+    auto all_read = [&](uint4 (&x)[kMoveUnroll]) {
+#pragma unroll
+      for (int i = 0; i < kMoveUnroll; ++i) asm volatile("" : "+r"(x[i].x), "+r"(x[i].y), "+r"(x[i].z), "+r"(x[i].w));
+      if (ctas > 1)
+        cluster_barrier_relaxed();
+      else
+        __syncthreads();
+    };
+    uint4 x0[kMoveUnroll], x1[kMoveUnroll];
+    Cursor in{0, 0, sh.slots + row0}, out = in;
+    load(x0, in);
+    while (out.round < rounds) {  // an even number of steps: keys and values
+      load(x1, in);
+      all_read(x0);
+      store(x0, out);
+      load(x0, in);
+      all_read(x1);
+      store(x1, out);
+    }
+    // Every CTA has read the stage's scores before the first barrier above.
+    for (int i = tid; i < rounds * round; i += kEvictThreads) {
+      const int j = lo + (((i >> log_round) * ctas + rank) << log_round) + (i & (round - 1));
+      if (j < n) wo[j] = sh.score[i];
+    }
   }
+  if (h == 0 && tid == 0 && rank == 0) a.new_lens[s] = n;
+  for (int j = n + rank * kEvictThreads + tid; j < a.budget; j += ctas * kEvictThreads) kept[j] = -1;
+  // The rest of the row starts from zero: every score has been read.
+  for (int j = n + rank * kEvictThreads + tid; j < a.score_stride; j += ctas * kEvictThreads) wo[j] = 0.f;
 }
 
 }  // namespace pa

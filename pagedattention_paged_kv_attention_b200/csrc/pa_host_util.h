@@ -41,21 +41,32 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // Launch with programmatic stream serialisation: the kernel may be scheduled while the previous kernel
 // in the stream is still running. Every kernel launched this way begins with grid_dependency_wait()
 // (pa_device.cuh) before any global-memory access, so stream order holds for memory and only the
-// launch latency and the shared-memory prologue overlap the previous kernel.
+// launch latency and the shared-memory prologue overlap the previous kernel. cluster: CTAs along x that
+// form a cluster.
 template <typename... Params, typename... Args>
-cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                              Args&&... args) {
-  cudaLaunchAttribute attr[1];
+cudaError_t launch_overlapped_clusters(unsigned cluster, void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                                       cudaStream_t stream, Args&&... args) {
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                              Args&&... args) {
+  return launch_overlapped_clusters(1, kernel, grid, block, smem, stream, std::forward<Args>(args)...);
 }
 
 // Ordinary launch (full stream serialisation) whose status is the launch's own: unlike <<<>>> followed
@@ -83,5 +94,16 @@ pa_status paged_attention_check(const void* out, const void* query, pa_dtype q_d
                                 const int32_t* context_lens, int num_seqs, int num_heads, int num_kv_heads,
                                 int head_size, int block_size, int num_blocks, int max_context_len, float scale,
                                 int partition_size, size_t* workspace_bytes, bool* empty);
+
+// Decode attention of one query row per sequence, found through q_start (pa_paged_cross_attention of single
+// tokens): the workspace of these sizes, whether the cache's layout is one that the decode kernel reads, and
+// the launch of a call whose arguments and workspace have been checked. Defined in pa_api.cu.
+size_t decode_rows_workspace(int num_seqs, int num_heads, int num_kv_heads, int head_size, int max_context_len);
+bool decode_rows_supported(int block_size, int num_blocks);
+pa_status decode_rows(void* out, const void* query, pa_dtype q_dtype, const void* key_cache, const void* value_cache,
+                      pa_dtype kv_dtype, const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                      int max_blocks_per_seq, const int32_t* context_lens, const int32_t* q_start, int num_seqs,
+                      int num_q_tokens, int num_heads, int num_kv_heads, int head_size, int block_size, int num_blocks,
+                      int max_context_len, float scale, void* workspace, pa_stream_t stream);
 
 }  // namespace pa_host

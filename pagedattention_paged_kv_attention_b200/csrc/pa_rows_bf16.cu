@@ -1,0 +1,10 @@
+// Decode attention over rows found by q_start (cross attention of single tokens), for bfloat16 queries.
+#include "pa_launch.cuh"
+
+namespace pa {
+cudaError_t launch_rows_bf16(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, bool fp8_cache, int D,
+                         int G, int grid, cudaStream_t stream) {
+  if (fp8_cache) return launch_attention<__nv_bfloat16, __nv_fp8_e4m3, kDecodeRows>(tk, tv, a, D, G, grid, stream);
+  return launch_attention<__nv_bfloat16, __nv_bfloat16, kDecodeRows>(tk, tv, a, D, G, grid, stream);
+}
+}  // namespace pa

@@ -209,8 +209,41 @@ def _same_scales(k_scale, v_scale):
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
+
+
+def _device(t, name):
+    """The current device, on which t has to be: the kernels run there, on its current stream."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    dev = torch.cuda.current_device()
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+    return dev
+
+
+def _operand(t, name, dtype, dim, dev):
+    """_arg for the calls of a decode step, whose host time counts: the pointer of a dense tensor of this type and
+    rank on the current device `dev`, where the kernels run. None passes through as a null pointer."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.get_device() != dev or t.dim() != dim or (dtype is not None and t.dtype != dtype) or not t.is_contiguous():
+        _arg(t, name, None if dtype is None else (dtype,), dim)
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+    return t.data_ptr()
+
+
+def _scale_operands(k_scale, v_scale, cache, dev):
+    """The pointers of an FP8 cache's scales ([Hkv], or [num_blocks, Hkv] for per-block scales)."""
+    if k_scale is None and v_scale is None:
+        return None, None
+    _same_scales(k_scale, v_scale)
+    _scales(k_scale, "k_scale", cache)
+    return _operand(k_scale, "k_scale", torch.float32, k_scale.dim(), dev), \
+        _operand(v_scale, "v_scale", torch.float32, k_scale.dim(), dev)
 
 
 def partition_size(num_seqs, num_heads, num_kv_heads, max_context_len, partition_size=0) -> int:
@@ -249,17 +282,16 @@ def paged_attention(out, query, key_cache, value_cache, block_tables, context_le
     return out
 
 
-def _check_batch(out, scores, query, key_cache, value_cache, block_tables, context_lens, k_scale, v_scale):
+def _check_batch(out, scores, query, key_cache, value_cache, block_tables, context_lens):
     """The shapes that must agree in a call over a batch of S sequences (scores: [S, Hkv, stride] or None)."""
     S, Hkv = context_lens.shape[0], key_cache.shape[2]
     _same(out, query, "out/query")
     _same(key_cache, value_cache, "key_cache/value_cache")
-    _same_scales(k_scale, v_scale)
-    if query.dim() != 3 or query.shape[2] != key_cache.shape[3]:
+    if query.shape[2] != key_cache.shape[3]:
         raise ValueError(f"query: expected [rows, heads, {key_cache.shape[3]}], got {tuple(query.shape)}")
-    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+    if block_tables.shape[0] != S:
         raise ValueError(f"block_tables: expected {S} rows, got {tuple(block_tables.shape)}")
-    if scores is not None and (scores.dim() != 3 or tuple(scores.shape[:2]) != (S, Hkv)):
+    if scores is not None and (scores.dim() != 3 or scores.shape[0] != S or scores.shape[1] != Hkv):
         raise ValueError(f"scores: expected ({S}, {Hkv}, stride), got {tuple(scores.shape)}")
 
 
@@ -283,20 +315,20 @@ def paged_attention_accumulate(out, scores, query, key_cache, value_cache, block
     its kv head, to scores[S,Hkv,stride] (float32)."""
     S, H, d = query.shape
     NB, bs, Hkv, _ = key_cache.shape
-    _check_batch(out, scores, query, key_cache, value_cache, block_tables, context_lens, k_scale, v_scale)
+    _check_batch(out, scores, query, key_cache, value_cache, block_tables, context_lens)
     if context_lens.shape[0] != S:
         raise ValueError(f"context_lens: expected {S} lengths, got {context_lens.shape[0]}")
-    args = (_arg(out, "out"), _arg(scores, "scores", _F32, 3), scores.shape[2], _arg(query, "query"),
-            dtype_code(query.dtype), _arg(key_cache, "key_cache"), _arg(value_cache, "value_cache"),
-            cache_code(key_cache, k_scale), _scales(k_scale, "k_scale", key_cache), _scales(v_scale, "v_scale", key_cache),
-            _arg(block_tables, "block_tables", _I32, 2), block_tables.shape[1],
-            _arg(context_lens, "context_lens", _I32, 1), S, H, Hkv, d, bs, NB, int(max_context_len), float(scale),
-            int(partition_size), _arg(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-            _stream(stream))
-    _on_current_device(out=out, scores=scores, query=query, key_cache=key_cache, value_cache=value_cache,
-                       block_tables=block_tables, context_lens=context_lens, workspace=workspace, k_scale=k_scale,
-                       v_scale=v_scale)
-    _check(lib.pa_paged_attention_accumulate(*args), "pa_paged_attention_accumulate")
+    dev = _device(query, "query")
+    ks, vs = _scale_operands(k_scale, v_scale, key_cache, dev)
+    st = lib.pa_paged_attention_accumulate(
+        _operand(out, "out", None, 3, dev), _operand(scores, "scores", torch.float32, 3, dev), scores.shape[2],
+        _operand(query, "query", None, 3, dev), dtype_code(query.dtype), _operand(key_cache, "key_cache", None, 4, dev),
+        _operand(value_cache, "value_cache", None, 4, dev), cache_code(key_cache, k_scale), ks, vs,
+        _operand(block_tables, "block_tables", torch.int32, 2, dev), block_tables.shape[1],
+        _operand(context_lens, "context_lens", torch.int32, 1, dev), S, H, Hkv, d, bs, NB, int(max_context_len),
+        float(scale), int(partition_size), _operand(workspace, "workspace", None, workspace.dim(), dev),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "pa_paged_attention_accumulate")
     return out
 
 
@@ -340,19 +372,20 @@ def paged_prefill_accumulate(out, scores, query, key_cache, value_cache, block_t
     T, H, d = query.shape
     NB, bs, Hkv, _ = key_cache.shape
     S = context_lens.shape[0]
-    _check_batch(out, scores, query, key_cache, value_cache, block_tables, context_lens, k_scale, v_scale)
+    _check_batch(out, scores, query, key_cache, value_cache, block_tables, context_lens)
     _check_chunks(q_start, S)
-    args = (_arg(out, "out"), _arg(scores, "scores", _F32, 3), scores.shape[2], _arg(query, "query"),
-            dtype_code(query.dtype), _arg(key_cache, "key_cache"), _arg(value_cache, "value_cache"),
-            cache_code(key_cache, k_scale), _scales(k_scale, "k_scale", key_cache), _scales(v_scale, "v_scale", key_cache),
-            _arg(block_tables, "block_tables", _I32, 2), block_tables.shape[1],
-            _arg(context_lens, "context_lens", _I32, 1), _arg(q_start, "q_start", _I32, 1), S, T, H, Hkv, d, bs, NB,
-            int(max_q_len), int(max_context_len), int(window), float(scale), _arg(workspace, "workspace"),
-            workspace.numel() * workspace.element_size(), _stream(stream))
-    _on_current_device(out=out, scores=scores, query=query, key_cache=key_cache, value_cache=value_cache,
-                       block_tables=block_tables, context_lens=context_lens, q_start=q_start, workspace=workspace,
-                       k_scale=k_scale, v_scale=v_scale)
-    _check(lib.pa_paged_prefill_accumulate(*args), "pa_paged_prefill_accumulate")
+    dev = _device(query, "query")
+    ks, vs = _scale_operands(k_scale, v_scale, key_cache, dev)
+    st = lib.pa_paged_prefill_accumulate(
+        _operand(out, "out", None, 3, dev), _operand(scores, "scores", torch.float32, 3, dev), scores.shape[2],
+        _operand(query, "query", None, 3, dev), dtype_code(query.dtype), _operand(key_cache, "key_cache", None, 4, dev),
+        _operand(value_cache, "value_cache", None, 4, dev), cache_code(key_cache, k_scale), ks, vs,
+        _operand(block_tables, "block_tables", torch.int32, 2, dev), block_tables.shape[1],
+        _operand(context_lens, "context_lens", torch.int32, 1, dev), _operand(q_start, "q_start", torch.int32, 1, dev),
+        S, T, H, Hkv, d, bs, NB, int(max_q_len), int(max_context_len), int(window), float(scale),
+        _operand(workspace, "workspace", None, workspace.dim(), dev), workspace.numel() * workspace.element_size(),
+        _stream(stream))
+    _check(st, "pa_paged_prefill_accumulate")
     return out
 
 
@@ -373,17 +406,19 @@ def paged_cross_attention(out, query, key_cache, value_cache, block_tables, cont
     T, H, d = query.shape
     NB, bs, Hkv, _ = key_cache.shape
     S = context_lens.shape[0]
-    _check_batch(out, None, query, key_cache, value_cache, block_tables, context_lens, k_scale, v_scale)
+    _check_batch(out, None, query, key_cache, value_cache, block_tables, context_lens)
     _check_chunks(q_start, S)
-    args = (_arg(out, "out"), _arg(query, "query"), dtype_code(query.dtype), _arg(key_cache, "key_cache"),
-            _arg(value_cache, "value_cache"), cache_code(key_cache, k_scale), _scales(k_scale, "k_scale", key_cache),
-            _scales(v_scale, "v_scale", key_cache), _arg(block_tables, "block_tables", _I32, 2), block_tables.shape[1],
-            _arg(context_lens, "context_lens", _I32, 1), _arg(q_start, "q_start", _I32, 1), S, T, H, Hkv, d, bs, NB,
-            int(max_q_len), int(max_context_len), float(scale), _arg(workspace, "workspace"),
-            workspace.numel() * workspace.element_size(), _stream(stream))
-    _on_current_device(out=out, query=query, key_cache=key_cache, value_cache=value_cache, block_tables=block_tables,
-                       context_lens=context_lens, q_start=q_start, workspace=workspace, k_scale=k_scale, v_scale=v_scale)
-    _check(lib.pa_paged_cross_attention(*args), "pa_paged_cross_attention")
+    dev = _device(query, "query")
+    ks, vs = _scale_operands(k_scale, v_scale, key_cache, dev)
+    st = lib.pa_paged_cross_attention(
+        _operand(out, "out", None, 3, dev), _operand(query, "query", None, 3, dev), dtype_code(query.dtype),
+        _operand(key_cache, "key_cache", None, 4, dev), _operand(value_cache, "value_cache", None, 4, dev),
+        cache_code(key_cache, k_scale), ks, vs, _operand(block_tables, "block_tables", torch.int32, 2, dev),
+        block_tables.shape[1], _operand(context_lens, "context_lens", torch.int32, 1, dev),
+        _operand(q_start, "q_start", torch.int32, 1, dev), S, T, H, Hkv, d, bs, NB, int(max_q_len),
+        int(max_context_len), float(scale), _operand(workspace, "workspace", None, workspace.dim(), dev),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "pa_paged_cross_attention")
     return out
 
 
@@ -422,27 +457,18 @@ def reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, k_scale=
     _check(st, "pa_reshape_and_cache")
 
 
-def _on_current_device(**tensors):
-    """Every tensor is on the current device: the kernels run there, on its current stream."""
-    dev = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
-
-
-def _token_rows(t, name, dtype):
+def _token_rows(t, name, dtype, dev):
     """Pointer and token stride of a [T, heads, d] tensor whose tokens are dense rows, possibly further
     apart than a row (a slice of a fused projection)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dim() != 3 or t.dtype != dtype:
-        raise ValueError(f"{name}: expected 3 dimensions of {dtype}, got shape {tuple(t.shape)} {t.dtype}")
     T, H, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
+    s0, s1, s2 = t.stride()
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
+    if (d > 1 and s2 != 1) or (H > 1 and s1 != d):
         raise ValueError(f"{name}: each token's [heads, head_size] row must be dense, got strides {t.stride()}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor")
-    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if T > 1 else H * d)
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: must be a CUDA tensor on the current device cuda:{dev}, got {t.device}")
+    return t.data_ptr(), (s0 if T > 1 else H * d)
 
 
 def rope_reshape_and_cache(query_out, query, key, value, key_cache, value_cache, slot_mapping, positions, inv_freq,
@@ -463,18 +489,17 @@ def rope_reshape_and_cache(query_out, query, key, value, key_cache, value_cache,
                          f"{tuple(slot_mapping.shape)}")
     if inv_freq.shape != freq_axis.shape:
         raise ValueError(f"inv_freq/freq_axis: lengths differ ({tuple(inv_freq.shape)} vs {tuple(freq_axis.shape)})")
-    _same_scales(k_scale, v_scale)
-    rows = [x for t, name in ((query_out, "query_out"), (query, "query"), (key, "key"), (value, "value"))
-            for x in _token_rows(t, name, query.dtype)]
-    args = (*rows, dtype_code(query.dtype), _arg(key_cache, "key_cache"), _arg(value_cache, "value_cache"),
-            cache_code(key_cache, k_scale), _scales(k_scale, "k_scale", key_cache), _scales(v_scale, "v_scale", key_cache),
-            _arg(slot_mapping, "slot_mapping", _I64, 1), _arg(positions, "positions", _I32, 2), positions.shape[0],
-            _arg(inv_freq, "inv_freq", _F32, 1), _arg(freq_axis, "freq_axis", _I32, 1), 2 * inv_freq.shape[0],
-            int(bool(interleaved)), T, H, Hkv, d, bs, NB, _stream(stream))
-    _on_current_device(query_out=query_out, query=query, key=key, value=value, key_cache=key_cache,
-                       value_cache=value_cache, slot_mapping=slot_mapping, positions=positions, inv_freq=inv_freq,
-                       freq_axis=freq_axis, k_scale=k_scale, v_scale=v_scale)
-    _check(lib.pa_rope_reshape_and_cache(*args), "pa_rope_reshape_and_cache")
+    dev, dt = _device(query, "query"), query.dtype
+    ks, vs = _scale_operands(k_scale, v_scale, key_cache, dev)
+    st = lib.pa_rope_reshape_and_cache(
+        *_token_rows(query_out, "query_out", dt, dev), *_token_rows(query, "query", dt, dev),
+        *_token_rows(key, "key", dt, dev), *_token_rows(value, "value", dt, dev), dtype_code(dt),
+        _operand(key_cache, "key_cache", None, 4, dev), _operand(value_cache, "value_cache", None, 4, dev),
+        cache_code(key_cache, k_scale), ks, vs, _operand(slot_mapping, "slot_mapping", torch.int64, 1, dev),
+        _operand(positions, "positions", torch.int32, 2, dev), positions.shape[0],
+        _operand(inv_freq, "inv_freq", torch.float32, 1, dev), _operand(freq_axis, "freq_axis", torch.int32, 1, dev),
+        2 * inv_freq.shape[0], int(bool(interleaved)), T, H, Hkv, d, bs, NB, _stream(stream))
+    _check(st, "pa_rope_reshape_and_cache")
     return query_out
 
 
@@ -502,17 +527,18 @@ def evict_tokens(kept, new_lens, scores_out, scores, key_cache, value_cache, blo
             dst_block_tables.shape[0] != S:
         raise ValueError(f"block tables: expected {S} rows, got {tuple(block_tables.shape)} and "
                          f"{tuple(dst_block_tables.shape)}")
-    args = (_arg(kept, "kept", _I32, 3), _arg(new_lens, "new_lens", _I32, 1), _arg(scores_out, "scores_out", _F32, 3),
-            _arg(scores, "scores", _F32, 3), scores.shape[2], _arg(key_cache, "key_cache"),
-            _arg(value_cache, "value_cache"), cache_code(key_cache, k_scale), _arg(block_tables, "block_tables", _I32, 2),
-            block_tables.shape[1], _arg(dst_block_tables, "dst_block_tables", _I32, 2), dst_block_tables.shape[1],
-            _arg(context_lens, "context_lens", _I32, 1), S, Hkv, d, bs, NB, int(max_context_len), int(budget),
-            int(num_sink), int(num_recent), _arg(workspace, "workspace"),
-            workspace.numel() * workspace.element_size(), _stream(stream))
-    _on_current_device(kept=kept, new_lens=new_lens, scores_out=scores_out, scores=scores, key_cache=key_cache,
-                       value_cache=value_cache, block_tables=block_tables, dst_block_tables=dst_block_tables,
-                       context_lens=context_lens, workspace=workspace)
-    _check(lib.pa_evict_tokens(*args), "pa_evict_tokens")
+    dev, i32 = _device(scores, "scores"), torch.int32
+    st = lib.pa_evict_tokens(
+        _operand(kept, "kept", i32, 3, dev), _operand(new_lens, "new_lens", i32, 1, dev),
+        _operand(scores_out, "scores_out", torch.float32, 3, dev), _operand(scores, "scores", torch.float32, 3, dev),
+        scores.shape[2], _operand(key_cache, "key_cache", None, 4, dev),
+        _operand(value_cache, "value_cache", None, 4, dev), cache_code(key_cache, k_scale),
+        _operand(block_tables, "block_tables", i32, 2, dev), block_tables.shape[1],
+        _operand(dst_block_tables, "dst_block_tables", i32, 2, dev), dst_block_tables.shape[1],
+        _operand(context_lens, "context_lens", i32, 1, dev), S, Hkv, d, bs, NB, int(max_context_len), int(budget),
+        int(num_sink), int(num_recent), _operand(workspace, "workspace", None, workspace.dim(), dev),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "pa_evict_tokens")
 
 
 def copy_blocks(key_cache, value_cache, block_mapping, stream=None):

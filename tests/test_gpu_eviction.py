@@ -67,6 +67,7 @@ def check(st, before, out, window=0, seqs=None):
         assert torch.equal(st["scores"][s, :, L:], before[s, :, L:])
         if n == 0 or L == 0:
             assert torch.equal(st["scores"][s], before[s])
+            assert out is None or bool((out[int(st["q_start"][s]):int(st["q_start"][s]) + n] == 0).all())
             continue
         rows = slice(int(st["q_start"][s]), int(st["q_start"][s]) + n)
         k, v = gather(st["k64"], st["table"], s, L, st["bs"]), gather(st["v64"], st["table"], s, L, st["bs"])
@@ -108,13 +109,14 @@ def test_step_against_the_formula(P, case):
     before = st["scores"].clone()
     out, plain = torch.full_like(st["q"], float("nan")), torch.empty_like(st["q"])
     ws = step(P, st, out, part=part)
-    ws2 = P.make_workspace(*st["q"].shape[:2], Hkv, d, st["max_len"], part)
-    P.paged_attention(plain, st["q"], st["kc"], st["vc"], st["table"], st["cl"], st["scale"], st["max_len"], ws2,
-                      k_scale=st["ks"], v_scale=st["vs"], partition_size=part)
     torch.cuda.synchronize()
     assert P.get_device_error(ws) == 0
-    assert torch.equal(out.view(torch.int16), plain.view(torch.int16))
-    check(st, before, None)
+    if part:  # left open, the two calls may choose different partitions
+        ws2 = P.make_workspace(*st["q"].shape[:2], Hkv, d, st["max_len"], part)
+        P.paged_attention(plain, st["q"], st["kc"], st["vc"], st["table"], st["cl"], st["scale"], st["max_len"], ws2,
+                          k_scale=st["ks"], v_scale=st["vs"], partition_size=part)
+        assert torch.equal(out.view(torch.int16), plain.view(torch.int16))
+    check(st, before, out)
     again = before.clone()
     step(P, st, out, ws=ws, part=part, scores=again)
     assert torch.equal(again, st["scores"])
