@@ -231,20 +231,23 @@ pa_status build_launch(AttnLaunch* l, const AttnPlan& plan, void* out, const voi
   return PA_OK;
 }
 
-// The partition size of the calls with their own workspaces when the caller leaves it open: plan_partition's,
-// or less when that leaves SMs without an item -- then as many partitions as give every SM one, of at least
-// kPartitionQuantum tokens. A batch of one reads 8 kv heads x 256 tokens through one SM otherwise, at a
-// fortieth of the card's bandwidth (one sequence of 701 tokens: 44 us; in partitions of 64: 18 us).
+// The partition size of the calls with their own workspaces when the caller leaves it open. About ten items
+// per CTA at max_context_len, as ragged batches hold half of that (32 sequences over up to 6404 states: 102 us
+// at plan_partition's 320 tokens, 91 us at 192; 128 of up to 4092 tokens: 252 and 244 us), of kMinAutoPartition
+// tokens at least; but where that leaves SMs without an item, as many as give every SM one. A batch of one
+// reads 8 kv heads x 256 tokens through one SM otherwise (one sequence of 701 tokens: 38 us; in partitions of
+// 64: 23 us).
 int plan_fine_partition(int num_seqs, int num_heads, int num_kv_heads, int max_context_len, int partition_size) {
-  const int ps = plan_partition(num_seqs, num_heads, num_kv_heads, max_context_len, partition_size);
-  if (ps <= 0 || partition_size > 0 || num_seqs == 0 || max_context_len == 0) return ps;
+  const int base = plan_partition(num_seqs, num_heads, num_kv_heads, max_context_len, partition_size);
+  if (base <= 0 || partition_size > 0 || num_seqs == 0 || max_context_len == 0) return base;
   int g_tile, subgroups;
   group_tiling(num_heads / num_kv_heads, &g_tile, &subgroups);
   const long long units = static_cast<long long>(num_seqs) * ceil_div(num_kv_heads, pa::kHeadBlock) * subgroups;
-  const long long parts = kPlanSMs / units;
-  if (parts <= ceil_div(max_context_len, ps)) return ps;
-  const long long fine = (max_context_len + parts - 1) / parts;
-  return std::min(ps, static_cast<int>(round_up(static_cast<size_t>(fine), pa::kPartitionQuantum)));
+  const long long ctx = max_context_len;
+  long long ps = std::max<long long>(ctx * units / (2 * kPlanItemsPerCta * kPlanSMs) + 1, kMinAutoPartition);
+  if (units * ((ctx + ps - 1) / ps) < kPlanSMs && units <= kPlanSMs) ps = (ctx * units + kPlanSMs - 1) / kPlanSMs;
+  ps = (ps + pa::kPartitionQuantum - 1) / pa::kPartitionQuantum * pa::kPartitionQuantum;
+  return static_cast<int>(std::min<long long>(base, ps));
 }
 
 // Workspace of pa_paged_attention_accumulate: that of pa_paged_attention, then the statistics and scaled
@@ -262,6 +265,15 @@ AccumulateLayout accumulate_layout(size_t base, int num_seqs, int num_heads, int
   w.logits = w.stats + round_up(rows * partitions * sizeof(float2), 256);
   w.total = w.logits + round_up(rows * w.stride * sizeof(float), 256);
   return w;
+}
+
+template <int U>
+cudaError_t launch_weights(const pa::AttnArgs& a, float* scores, int score_stride, int max_context_len,
+                           cudaStream_t st) {
+  const unsigned chunks = static_cast<unsigned>(ceil_div(max_context_len, pa::kWeightTokens));
+  const unsigned heads = static_cast<unsigned>(a.num_kv_heads), seqs = static_cast<unsigned>(a.num_seqs);
+  return pa_host::launch_overlapped(pa::attention_weights_kernel<U>, dim3(chunks, heads, seqs),
+                                    dim3(pa::kWeightThreads), 0, st, a, scores, static_cast<long long>(score_stride));
 }
 
 }  // namespace
@@ -433,10 +445,11 @@ pa_status pa_paged_attention_accumulate(void* out, float* scores, int score_stri
   if (e == cudaSuccess && plan.partitions > 1)
     e = bf16 ? pa::launch_reduce_bf16(l.a, head_size, st) : pa::launch_reduce_f16(l.a, head_size, st);
   if (e == cudaSuccess && max_context_len > 0) {
-    const unsigned chunks = static_cast<unsigned>(ceil_div(max_context_len, pa::kWeightTokens));
-    e = pa_host::launch_overlapped(pa::attention_weights_kernel,
-                                   dim3(chunks, static_cast<unsigned>(num_kv_heads), static_cast<unsigned>(num_seqs)),
-                                   dim3(pa::kWeightThreads), 0, st, l.a, scores, static_cast<long long>(score_stride));
+    const int group = num_heads / num_kv_heads;
+    e = group == 1   ? launch_weights<1>(l.a, scores, score_stride, max_context_len, st)
+        : group == 2 ? launch_weights<2>(l.a, scores, score_stride, max_context_len, st)
+        : group <= 4 ? launch_weights<4>(l.a, scores, score_stride, max_context_len, st)
+                     : launch_weights<8>(l.a, scores, score_stride, max_context_len, st);
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

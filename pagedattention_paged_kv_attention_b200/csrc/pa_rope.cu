@@ -2,7 +2,7 @@
 // and the launch of pa::rope_reshape_and_cache_kernel (pa_rope.cuh).
 #include <cuda_runtime.h>
 
-#include <type_traits>
+#include <algorithm>
 
 #include "pa_host_util.h"
 #include "pa_rope.cuh"
@@ -19,11 +19,14 @@ constexpr int64_t kMaxRowElems = int64_t(1) << 24;  // elements of one token's r
 template <typename T, typename KVT>
 cudaError_t launch_rope(const pa::RopeArgs& a, bool interleaved, cudaStream_t st) {
   const unsigned tokens = static_cast<unsigned>(a.num_tokens);
+  const int64_t units = static_cast<int64_t>(a.num_heads + a.num_kv_heads) * a.units +
+                        static_cast<int64_t>(a.num_kv_heads) * a.head_size / 8;
+  const unsigned threads = static_cast<unsigned>(std::min<int64_t>(pa::kRopeThreads, (units + 31) / 32 * 32));
   if (interleaved)
     return pa_host::launch_overlapped(pa::rope_reshape_and_cache_kernel<T, KVT, true>, dim3(tokens),
-                                      dim3(pa::kRopeThreads), 0, st, a);
+                                      dim3(threads), 0, st, a);
   return pa_host::launch_overlapped(pa::rope_reshape_and_cache_kernel<T, KVT, false>, dim3(tokens),
-                                    dim3(pa::kRopeThreads), 0, st, a);
+                                    dim3(threads), 0, st, a);
 }
 
 }  // namespace
@@ -57,8 +60,8 @@ extern "C" pa_status pa_rope_reshape_and_cache(
   const bool fp8 = pa_host::is_fp8(kv_dtype);
   if (fp8 && (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4))) return PA_ERR_INVALID_ARGUMENT;
   if (!fp8 && kv_dtype != in_dtype) return PA_ERR_UNSUPPORTED;
-  if (head_size % 8 != 0 || rotary_size % 16 != 0 || rotary_size > pa::kRopeMaxRotary || q_row > kMaxRowElems ||
-      kv_row > kMaxRowElems)
+  if (head_size % 8 != 0 || rotary_size % 16 != 0 || rotary_size > pa::kRopeMaxRotary ||
+      head_size > pa::kRopeMaxHead || q_row > kMaxRowElems || kv_row > kMaxRowElems)
     return PA_ERR_UNSUPPORTED;
   if (query_out_stride % 8 != 0 || query_stride % 8 != 0 || key_stride % 8 != 0 || value_stride % 8 != 0)
     return PA_ERR_UNSUPPORTED;
@@ -86,6 +89,10 @@ extern "C" pa_status pa_rope_reshape_and_cache(
   a.num_kv_heads = num_kv_heads;
   a.head_size = head_size;
   a.rotary = rotary_size;
+  a.units = rotary_size / (interleaved ? 8 : 16) + (head_size - rotary_size) / 8;
+  auto reciprocal = [](int n) { return static_cast<unsigned>(((uint64_t(1) << 32) + n - 1) / n); };
+  a.inv_units = reciprocal(a.units);
+  a.inv_plain = reciprocal(head_size / 8);
   a.block_size = block_size;
   a.num_blocks = num_blocks;
   a.scale_stride = pa_host::scale_block_stride(kv_dtype, num_kv_heads);

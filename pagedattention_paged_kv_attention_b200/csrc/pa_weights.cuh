@@ -15,11 +15,14 @@
 
 namespace pa {
 
-constexpr int kWeightThreads = 256;
-constexpr int kWeightTokens = 1024;    // tokens of one CTA
-constexpr int kWeightHeads = 64;       // query heads whose statistics are joined at a time
+constexpr int kWeightThreads = 128;
+constexpr int kWeightRound = 4 * kWeightThreads;   // tokens of a CTA's round, 4 consecutive ones a thread
+constexpr int kWeightTokens = 4 * kWeightRound;    // tokens of one CTA
+constexpr int kWeightHeads = 64;                   // query heads whose statistics are joined at a time
 
-// grid (token chunks, kv heads, sequences)
+// grid (token chunks, kv heads, sequences). U: heads whose scores a thread has in flight. The first ones' scores and
+// sums are fetched beside the statistics, so a CTA's first round costs one chain of loads.
+template <int U>
 __global__ void __launch_bounds__(kWeightThreads)
 attention_weights_kernel(const AttnArgs a, float* __restrict__ scores, long long score_stride) {
   __shared__ float lse[kWeightHeads];
@@ -29,17 +32,31 @@ attention_weights_kernel(const AttnArgs a, float* __restrict__ scores, long long
   const int L = a.context_lens[s];
   const long long t0 = static_cast<long long>(blockIdx.x) * kWeightTokens;
   if (L <= 0 || context_len_invalid(L, a) || t0 >= L) return;
+  const int left = static_cast<int>(min(static_cast<long long>(kWeightTokens), L - t0));
   const int n_parts = (L - 1) / a.partition_size + 1;
-  constexpr int kPer = kWeightTokens / kWeightThreads;
-  float acc[kPer];
+  const size_t row0 = static_cast<size_t>(s) * a.num_heads + static_cast<size_t>(kvh) * a.group;
+  // Rows of scores are padded to a multiple of 64, so the 16-byte reads past L stay inside them.
+  const float* z = a.logits + row0 * a.logit_stride + t0;
+  float* out = scores + (static_cast<size_t>(s) * a.num_kv_heads + kvh) * score_stride + t0;
+  float4 zv[U];
+  float old[4];
+  auto fetch = [&](int g, int t) {
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+    for (int u = 0; u < U; ++u)
+      if (t < left && g + u < a.group) zv[u] = *reinterpret_cast<const float4*>(z + (g + u) * a.logit_stride + t);
+  };
+  auto fetch_old = [&](int t) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) old[k] = t + k < left ? out[t + k] : 0.f;
+  };
+  int t = 4 * static_cast<int>(threadIdx.x);
+  fetch(0, t);
+  fetch_old(t);
   for (int g0 = 0; g0 < a.group; g0 += kWeightHeads) {
     const int heads = min(kWeightHeads, a.group - g0);
-    const size_t row0 = static_cast<size_t>(s) * a.num_heads + static_cast<size_t>(kvh) * a.group + g0;
     if (g0 > 0) __syncthreads();
     for (int g = warp; g < heads; g += kWeightThreads / 32) {
-      const float2* st = a.stats + (row0 + g) * a.num_partitions;
+      const float2* st = a.stats + (row0 + g0 + g) * a.num_partitions;
       float M = -INFINITY;
       for (int p = lane; p < n_parts; p += 32) M = fmaxf(M, st[p].x);
 #pragma unroll
@@ -51,17 +68,28 @@ attention_weights_kernel(const AttnArgs a, float* __restrict__ scores, long long
       if (lane == 0) lse[g] = M + log2f(sum);
     }
     __syncthreads();
-    const float* z = a.logits + row0 * a.logit_stride + t0 + threadIdx.x;
-    for (int g = 0; g < heads; ++g, z += a.logit_stride) {
+    for (t = 4 * static_cast<int>(threadIdx.x); t < left; t += kWeightRound) {
+      const bool first = g0 == 0 && t < kWeightRound;
+      if (!first) fetch_old(t);
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int g = 0; g < heads; g += U) {
+        if (!first || g > 0) fetch(g0 + g, t);
 #pragma unroll
-      for (int k = 0; k < kPer; ++k)
-        if (t0 + threadIdx.x + k * kWeightThreads < L) acc[k] += fast_exp2(z[k * kWeightThreads] - lse[g]);
+        for (int u = 0; u < U; ++u) {
+          if (g + u < heads) {
+            const float e = lse[g + u];
+            acc[0] += fast_exp2(zv[u].x - e);
+            acc[1] += fast_exp2(zv[u].y - e);
+            acc[2] += fast_exp2(zv[u].z - e);
+            acc[3] += fast_exp2(zv[u].w - e);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (t + k < left) out[t + k] = old[k] + acc[k];
     }
   }
-  float* out = scores + (static_cast<size_t>(s) * a.num_kv_heads + kvh) * score_stride + t0 + threadIdx.x;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k)
-    if (t0 + threadIdx.x + k * kWeightThreads < L) out[k * kWeightThreads] += acc[k];
 }
 
 }  // namespace pa

@@ -93,6 +93,9 @@ CASES = [
     dict(T=40, H=8, Hkv=8, d=128, r=128, axes=3, bs=16, cache="fp8", far=900000),
     dict(T=41, H=16, Hkv=2, d=128, r=64, axes=2, bs=8, cache="fp8_block", il=True, dtype="f16"),
     dict(T=9, H=2, Hkv=2, d=520, r=512, axes=3, bs=16, cache="fp8", dtype="f16", fused=True),
+    dict(T=5, H=3, Hkv=3, d=16, r=16, axes=1, bs=8),
+    dict(T=5, H=70, Hkv=1, d=16, r=16, axes=2, bs=8, il=True),
+    dict(T=3, H=2, Hkv=1, d=8192, r=512, axes=2, bs=2),
     dict(T=3000, H=4, Hkv=2, d=128, r=128, axes=3, bs=16),
 ]
 
