@@ -55,7 +55,8 @@ pa_status pa_paged_prefill_accumulate(void* out, float* scores, int score_stride
   if (checked != PA_OK || empty) return checked;
   if (!scores || !pa_host::aligned(scores, 4)) return PA_ERR_INVALID_ARGUMENT;
   const int key_tiles = pa_host::ceil_div(max_context_len, pa::pf::kKvTile);
-  if (key_tiles > 65535) return PA_ERR_UNSUPPORTED;
+  const int64_t items = static_cast<int64_t>(key_tiles) * num_seqs * num_kv_heads;
+  if (items > 0x3fffffff) return PA_ERR_UNSUPPORTED;
   pa_host::PrefillLaunch l;
   const pa_status built = pa_host::build_prefill(
       &l, out, query, key_cache, value_cache, kv_dtype, k_scale, v_scale, block_tables, max_blocks_per_seq,
@@ -72,8 +73,12 @@ pa_status pa_paged_prefill_accumulate(void* out, float* scores, int score_stride
     wa.score_stride = score_stride;
     wa.lse = l.a.lse;
     wa.window = window;
-    const dim3 grid(static_cast<unsigned>(num_kv_heads), static_cast<unsigned>(num_seqs),
-                    static_cast<unsigned>(key_tiles));
+    wa.num_items = static_cast<unsigned>(items);
+    int device = 0, sms = 0;
+    if (cudaGetDevice(&device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || sms <= 0)
+      return PA_ERR_CUDA;
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(sms, items)));
     e = q_dtype == PA_BF16 ? launch_weights<__nv_bfloat16>(l, wa, grid, kv_dtype, head_size, st)
                            : launch_weights<__half>(l, wa, grid, kv_dtype, head_size, st);
   }
