@@ -17,7 +17,7 @@ cudaError_t launch_weights_one(const pa_host::PrefillLaunch& l, const pa::pf::We
   const int smem = static_cast<int>(pa::pf::WLayout<D>::kBytes);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return pa_host::launch_plain(kernel, grid, dim3(pa::pf::kThreads), static_cast<size_t>(smem), st, l.tq, l.tk, l.a,
+  return pa_host::launch_plain(kernel, grid, dim3(pa::pf::kWThreads), static_cast<size_t>(smem), st, l.tq, l.tk, l.a,
                                wa);
 }
 
@@ -74,6 +74,8 @@ pa_status pa_paged_prefill_accumulate(void* out, float* scores, int score_stride
     wa.lse = l.a.lse;
     wa.window = window;
     wa.num_items = static_cast<unsigned>(items);
+    const int counted = window > 0 ? std::min(window, max_q_len) : max_q_len;
+    wa.draw = pa_host::ceil_div(counted, l.a.tile_tokens) > pa::pf::kDealTiles;
     int device = 0, sms = 0;
     if (cudaGetDevice(&device) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || sms <= 0)
