@@ -95,6 +95,21 @@ PA_API pa_status pa_bm_plan_decode(pa_block_manager* bm, const int64_t* seq_ids,
                                    int64_t* cow_pairs_out, int* num_cow_out, int32_t* tables_out, int max_blocks,
                                    int32_t pad, int32_t* context_lens_out);
 
+/*
+ * The plan of pa_evict_tokens for the n resident sequences seq_ids[0..n) (distinct), which are cut to at most
+ * budget >= 1 tokens each. tables_out ([n][max_blocks]) and context_lens_out receive the tables and lengths
+ * that hold the tokens now, dst_tables_out ([n][max_dst_blocks]) the blocks that hold them afterwards: a cut
+ * sequence keeps its own first ceil(budget / block_size) blocks, except that each block it shares is replaced
+ * by a fresh one (eviction moves rows, which the other owners still read where they were). Sequences within
+ * the budget keep their blocks, shared ones too. The manager's state becomes that after the eviction: run
+ * pa_evict_tokens before anything that writes the cache. Entries past a table are `pad`. INVALID_ARGUMENT if a
+ * sequence needs more than max_blocks or max_dst_blocks entries or is not resident; OUT_OF_BLOCKS when the
+ * pool has too few free blocks for the replacements (blocks given up by the call do not count).
+ */
+PA_API pa_status pa_bm_plan_evict(pa_block_manager* bm, const int64_t* seq_ids, int n, int64_t budget,
+                                  int32_t* tables_out, int max_blocks, int32_t* dst_tables_out, int max_dst_blocks,
+                                  int32_t pad, int32_t* context_lens_out);
+
 /* Releases a sequence, resident or swapped out. */
 PA_API pa_status pa_bm_free_sequence(pa_block_manager* bm, int64_t seq_id);
 

@@ -278,8 +278,8 @@ PA_API size_t pa_paged_prefill_accumulate_workspace_size(int num_q_tokens, int n
  *  max_context_len  >= every context_lens[s]; sizes the grid.
  *  workspace      >= pa_paged_prefill_accumulate_workspace_size(...) bytes, its header zeroed once.
  * Everything else is as in pa_paged_prefill. Weights are formed in fp32 from the unrounded scores. A chunk
- * outside its context, or a length past max_context_len (PA_DEVERR_CONTEXT_LEN), leaves the sequence's scores
- * as they are; tokens seen by a counted row that also sees a block outside the pool (PA_DEVERR_BLOCK_ID) get NaN.
+ * outside its context, a chunk that max_q_len's grid does not cover, or a length past max_context_len
+ * (PA_DEVERR_CONTEXT_LEN) leaves the sequence's scores as they are; tokens seen by a counted row that also sees a block outside the pool (PA_DEVERR_BLOCK_ID) get NaN.
  */
 PA_API pa_status pa_paged_prefill_accumulate(void* out, float* scores, int score_stride, const void* query,
                                              pa_dtype q_dtype, const void* key_cache, const void* value_cache,
@@ -311,8 +311,9 @@ PA_API size_t pa_paged_cross_attention_workspace_size(int num_seqs, int num_q_to
  *  max_q_len        >= every q_start[s+1] - q_start[s]; max_context_len >= every E_s. Both size the grid.
  *  workspace        >= pa_paged_cross_attention_workspace_size(...) bytes, its header zeroed once.
  * Types, layouts and supported sizes as in pa_paged_prefill. A negative E_s, or one past the block table or
- * past max_context_len, sets PA_DEVERR_CONTEXT_LEN and NaNs the sequence's rows; a block id outside the pool
- * sets PA_DEVERR_BLOCK_ID.
+ * past max_context_len, sets PA_DEVERR_CONTEXT_LEN and NaNs the sequence's rows, as does a chunk longer than
+ * max_q_len's grid covers (its rows past the grid, or all of them at max_q_len 1, are not written); a block id
+ * outside the pool sets PA_DEVERR_BLOCK_ID.
  */
 PA_API pa_status pa_paged_cross_attention(void* out, const void* query, pa_dtype q_dtype, const void* key_cache,
                                           const void* value_cache, pa_dtype kv_dtype, const float* k_scale,
@@ -368,7 +369,7 @@ PA_API pa_status pa_reshape_and_cache(const void* key, const void* value, pa_dty
  *  query          rows of [num_heads][head_size]; key, value: rows of [num_kv_heads][head_size]; in_dtype.
  *                 Strides are elements between tokens: at least a row (slices of one fused projection
  *                 are fine), multiples of 8.
- *  key_cache, value_cache, k_scale, v_scale, slot_mapping   as in pa_reshape_and_cache.
+ *  key_cache, value_cache, k_scale, v_scale, slot_mapping   as in pa_reshape_and_cache (slots are distinct).
  *  positions      [num_axes][num_tokens] int32 (negative positions turn backwards).
  *  inv_freq       [rotary_size / 2] fp32, the angle per position of each pair.
  *  freq_axis      [rotary_size / 2] int32; a pair whose axis is outside [0, num_axes) is not turned.

@@ -111,6 +111,18 @@ class BlockManager:
                                     _host_out(lens, np.int32, n, "lens")), "pa_bm_plan_decode")
         return slots, cow[:k.value], tables, lens
 
+    def plan_evict(self, seq_ids, budget: int, max_blocks: int, max_dst_blocks: int, pad: int = 0):
+        """The plan of evict_tokens: returns (tables [n, max_blocks], dst_tables [n, max_dst_blocks],
+        context_lens [n]), all int32, and cuts the sequences to at most `budget` tokens in the manager."""
+        ids = np.ascontiguousarray(seq_ids, np.int64)
+        n = len(ids)
+        tables = np.empty((n, max(max_blocks, 1)), np.int32)
+        dst = np.empty((n, max(max_dst_blocks, 1)), np.int32)
+        lens = np.empty(max(n, 1), np.int32)
+        _call(lib.pa_bm_plan_evict(self._h, ids.ctypes.data, n, budget, tables.ctypes.data, max_blocks,
+                                   dst.ctypes.data, max_dst_blocks, pad, lens.ctypes.data), "pa_bm_plan_evict")
+        return tables[:, :max_blocks], dst[:, :max_dst_blocks], lens[:n]
+
     def free_sequence(self, seq_id: int):
         _call(lib.pa_bm_free_sequence(self._h, seq_id), "pa_bm_free_sequence")
 

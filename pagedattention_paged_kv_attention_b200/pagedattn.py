@@ -32,7 +32,7 @@ EXPORTS = (
     "pa_paged_cross_attention_workspace_size", "pa_paged_cross_attention",
     # include/pa_block_manager.h
     "pa_bm_create", "pa_bm_destroy", "pa_bm_add_sequence", "pa_bm_fork", "pa_bm_append_slots",
-    "pa_bm_block_tables", "pa_bm_plan_decode", "pa_bm_free_sequence", "pa_bm_swap_out", "pa_bm_swap_in",
+    "pa_bm_block_tables", "pa_bm_plan_decode", "pa_bm_plan_evict", "pa_bm_free_sequence", "pa_bm_swap_out", "pa_bm_swap_in",
     "pa_bm_num_free_blocks", "pa_bm_sequence_info", "pa_bm_ref_count",
     # include/pa_probe.h
     "pa_probe_stream_read", "pa_probe_paged_read",
@@ -109,6 +109,8 @@ lib.pa_bm_block_tables.restype = _i
 lib.pa_bm_block_tables.argtypes = [_p, _p, _i, _p, _i, ctypes.c_int32, _p]
 lib.pa_bm_plan_decode.restype = _i
 lib.pa_bm_plan_decode.argtypes = [_p, _p, _i, _p, _p, _ip, _p, _i, ctypes.c_int32, _p]
+lib.pa_bm_plan_evict.restype = _i
+lib.pa_bm_plan_evict.argtypes = [_p, _p, _i, _i64, _p, _i, _p, _i, ctypes.c_int32, _p]
 lib.pa_bm_free_sequence.restype = _i
 lib.pa_bm_free_sequence.argtypes = [_p, _i64]
 lib.pa_bm_swap_out.restype = _i

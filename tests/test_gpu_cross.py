@@ -112,6 +112,29 @@ def test_invalid_lengths_are_flagged_and_their_rows_are_nan(P, chunks):
     check(st, out, seqs={3})
 
 
+def test_a_chunk_longer_than_announced_is_flagged(P):
+    st = make([300, 700], [3, 1], 8, 2, 128, 16, seed=4)           # three rows where one is announced
+    out = torch.zeros_like(st["q"])
+    ws = call(P, st, out, max_q=1)
+    torch.cuda.synchronize()
+    assert P.get_device_error(ws) == P.PA_DEVERR_CONTEXT_LEN
+    check(st, out, seqs={1})
+    assert bool((out[:3] == 0).all())
+    st = make([300, 2000], [300, 40], 8, 8, 128, 16, seed=4)       # 256 rows are covered
+    out = torch.zeros_like(st["q"])
+    ws = call(P, st, out, max_q=40)
+    torch.cuda.synchronize()
+    assert P.get_device_error(ws) == P.PA_DEVERR_CONTEXT_LEN
+    assert bool(out[:256].isnan().all()) and bool((out[256:300] == 0).all())
+    check(st, out, seqs={1})
+    st = make([3000, 300], [60, 40], 8, 8, 128, 16, seed=4)        # more than announced, but covered: computed
+    out = torch.zeros_like(st["q"])
+    ws = call(P, st, out, ws=P.make_cross_workspace(2, 100, 8, 8, 128, 40, 3000), max_q=40)
+    torch.cuda.synchronize()
+    assert P.get_device_error(ws) == 0
+    check(st, out)
+
+
 @pytest.mark.parametrize("n", [1, 5])
 def test_results_repeat_and_do_not_depend_on_the_other_sequences(P, n):
     st = make([1900, 33, 800], [n, n, n], 16, 4, 128, 16, seed=6)

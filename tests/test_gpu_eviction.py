@@ -206,6 +206,36 @@ def test_invalid_lengths_leave_the_scores(P):
     check(st, before, None, seqs={2})
 
 
+def test_empty_contexts_and_chunks(P):
+    """A padded decode batch whose sequences are all empty, and a prompt call without any new token."""
+    st = make([0, 0], None, 8, 2, 128, 16, seed=1)
+    before = st["scores"].clone()
+    out = torch.full_like(st["q"], 7.0)
+    ws = step(P, st, out)
+    torch.cuda.synchronize()
+    assert P.get_device_error(ws) == 0 and bool((out == 0).all()) and torch.equal(st["scores"], before)
+    st = make([90, 40], [0, 0], 8, 2, 128, 16, tail=3, seed=2)
+    before = st["scores"].clone()
+    out = torch.full_like(st["q"], 7.0)
+    st["chunks"] = [1]                               # max_q_len 1
+    ws = prompt(P, st, out)
+    torch.cuda.synchronize()
+    assert P.get_device_error(ws) == 0 and bool((out == 7).all()) and torch.equal(st["scores"], before)
+
+
+def test_a_chunk_longer_than_announced_leaves_the_scores(P):
+    st = make([300, 90], [300, 40], 8, 8, 128, 16, seed=7)
+    before = st["scores"].clone()
+    out = torch.zeros_like(st["q"])
+    ws = P.make_prefill_accumulate_workspace(340, 8)
+    P.paged_prefill_accumulate(out, st["scores"], st["q"], st["kc"], st["vc"], st["table"], st["cl"], st["q_start"],
+                               st["scale"], 40, 300, ws)
+    torch.cuda.synchronize()
+    assert P.get_device_error(ws) == P.PA_DEVERR_CONTEXT_LEN
+    assert torch.equal(st["scores"][0], before[0])
+    check(st, before, out, seqs={1})
+
+
 def test_blocks_outside_the_pool_make_the_scores_nan(P):
     st = make([200, 90], [200, 90], 8, 2, 128, 16, seed=6)
     before = st["scores"].clone()
@@ -476,3 +506,60 @@ def test_serving_loop(P, graph):
             cut()
             cut_reference(was, was_lens)
     assert P.get_device_error(ws) == 0 and P.get_device_error(pws) == 0 and P.get_device_error(ews) == 0
+
+
+def test_prefill_step_evict_with_the_block_manager(P):
+    """Sequences that share a prompt's blocks are cut by the manager's plan: shared blocks are replaced, the prompt's
+    owner keeps its tokens, freed blocks come back, and decoding goes on over what was kept."""
+    from pagedattention_paged_kv_attention_b200.block_manager import BlockManager
+    gen = torch.Generator(device="cuda").manual_seed(33)
+    H, Hkv, d, bs, NB, budget, dt = 4, 2, 64, 8, 64, 20, torch.float16
+    bm = BlockManager(NB, bs)
+    kc, vc = (torch.full((NB, bs, Hkv, d), float("nan"), dtype=dt, device="cuda") for _ in range(2))
+    randn = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(dt)  # noqa: E731
+    slots = torch.from_numpy(bm.add_sequence(0, 50).copy()).cuda()
+    k, v = randn(50, Hkv, d), randn(50, Hkv, d)
+    P.reshape_and_cache(k, v, kc, vc, slots)
+    bm.fork(0, 1)
+    s2 = torch.from_numpy(bm.add_sequence(2, 30, 0, 24).copy()).cuda()  # shares 3 blocks
+    k2, v2 = randn(30, Hkv, d), randn(30, Hkv, d)
+    k2[:24], v2[:24] = k[:24], v[:24]
+    P.reshape_and_cache(k2[24:].contiguous(), v2[24:].contiguous(), kc, vc, s2)
+    logical = {0: (k, v), 1: (k, v), 2: (k2, v2)}
+    free = bm.num_free_blocks()[0]
+    tables, dst, lens = bm.plan_evict([1, 2], budget, 8, 3)
+    assert lens.tolist() == [50, 30]
+    assert bm.sequence_info(1) == (20, 3, False) and bm.sequence_info(2) == (20, 3, False)
+    # 6 shared blocks are replaced; sequence 0 owns all its blocks alone now; one block of sequence 2 is free again
+    assert bm.num_free_blocks()[0] == free - 6 + 1
+    scores = torch.rand(2, Hkv, 56, generator=gen, device="cuda")
+    kept = torch.zeros(2, Hkv, budget, dtype=torch.int32, device="cuda")
+    new = torch.zeros(2, dtype=torch.int32, device="cuda")
+    cuda = lambda a: torch.from_numpy(a.copy()).cuda()  # noqa: E731
+    was = scores.clone()
+    P.evict_tokens(kept, new, scores, scores, kc, vc, cuda(tables), cuda(dst), cuda(lens), budget, 2, 5, 56,
+                   P.make_evict_workspace())
+    assert new.tolist() == [20, 20]
+    t0, l0 = bm.block_tables([0], 8)
+    assert l0.tolist() == [50]
+    assert torch.equal(gather(kc, cuda(t0), 0, 50, bs), k)             # the prompt's owner reads what it wrote
+    slots, cow, tables, lens = bm.plan_decode([1, 2], 8)
+    assert len(cow) == 0 and lens.tolist() == [21, 21]
+    nk, nv, q = randn(2, Hkv, d), randn(2, Hkv, d), randn(2, H, d)
+    P.reshape_and_cache(nk, nv, kc, vc, cuda(slots))
+    out = torch.empty_like(q)
+    before = scores.clone()
+    P.paged_attention_accumulate(out, scores, q, kc, vc, cuda(tables), cuda(lens), 0.125, 21,
+                                 P.make_accumulate_workspace(2, H, Hkv, d, 21))
+    for i, s in enumerate((1, 2)):
+        per = []
+        for h in range(Hkv):
+            ids = evict(was[i, h], len(logical[s][0]), budget, 2, 5)
+            assert kept[i, h].tolist() == ids
+            per.append(torch.tensor(ids, device="cuda"))
+        keys, values = (torch.cat([torch.stack([logical[s][w][per[h], h] for h in range(Hkv)], 1), x[i:i + 1]]).double()
+                        for w, x in ((0, nk), (1, nv)))
+        ref, bound, add, rel = attention(q[i:i + 1], keys, values, None, 0.125, True, 1, (dt, "16"))
+        assert bool((out[i:i + 1].double() - ref).abs().le(bound).all())
+        err = (scores[i, :, :21] - before[i, :, :21]).double() - add
+        assert bool(err.abs().le(rel * add + 2 * U * (before[i, :, :21].double() + add)).all())
