@@ -211,7 +211,7 @@ def _same_scales(k_scale, v_scale):
 
 def _stream(stream):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -284,17 +284,51 @@ def paged_attention(out, query, key_cache, value_cache, block_tables, context_le
     return out
 
 
-def _check_batch(out, scores, query, key_cache, value_cache, block_tables, context_lens):
-    """The shapes that must agree in a call over a batch of S sequences (scores: [S, Hkv, stride] or None)."""
-    S, Hkv = context_lens.shape[0], key_cache.shape[2]
-    _same(out, query, "out/query")
-    _same(key_cache, value_cache, "key_cache/value_cache")
-    if query.shape[2] != key_cache.shape[3]:
-        raise ValueError(f"query: expected [rows, heads, {key_cache.shape[3]}], got {tuple(query.shape)}")
-    if block_tables.shape[0] != S:
-        raise ValueError(f"block_tables: expected {S} rows, got {tuple(block_tables.shape)}")
-    if scores is not None and (scores.dim() != 3 or scores.shape[0] != S or scores.shape[1] != Hkv):
-        raise ValueError(f"scores: expected ({S}, {Hkv}, stride), got {tuple(scores.shape)}")
+def _refuse(where, **operands):
+    """Raises for the first operand that its call cannot take; operands: name=(tensor, dtype or None, rank)."""
+    dev = None
+    for name, (t, dtype, dim) in operands.items():
+        if t is not None and not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+        dev = _device(t, name) if dev is None else dev
+        _operand(t, name, dtype, dim, dev)
+    raise ValueError(f"{where}: the arguments' shapes do not fit together: " +
+                     ", ".join(f"{name} {tuple(t.shape)} {t.dtype}" for name, (t, _, _) in operands.items()))
+
+
+def _batch(where, out, scores, query, key_cache, value_cache, block_tables, context_lens, workspace, q_start=None):
+    """(device, query shape, cache shape, sequences) of a call over a batch, after the checks that _arg and _same make.
+    They stand in one expression because a decode step's host time counts; what fails is found by _refuse."""
+    try:
+        dev, qs, ks, dt, ct = query.get_device(), query.shape, key_cache.shape, query.dtype, key_cache.dtype
+        S, = context_lens.shape
+        ok = (len(qs) == 3 and len(ks) == 4 and qs[2] == ks[3] and dev >= 0 and dev == torch._C._cuda_getDevice() and
+              out.shape == qs and out.dtype == dt and value_cache.shape == ks and value_cache.dtype == ct and
+              block_tables.dtype == torch.int32 and context_lens.dtype == torch.int32 and
+              block_tables.dim() == 2 and block_tables.shape[0] == S and
+              out.get_device() == dev and key_cache.get_device() == dev and value_cache.get_device() == dev and
+              block_tables.get_device() == dev and context_lens.get_device() == dev and
+              workspace.get_device() == dev and query.is_contiguous() and out.is_contiguous() and
+              key_cache.is_contiguous() and value_cache.is_contiguous() and block_tables.is_contiguous() and
+              context_lens.is_contiguous() and workspace.is_contiguous())
+        if ok and scores is not None:
+            ss = scores.shape
+            ok = (len(ss) == 3 and ss[0] == S and ss[1] == ks[2] and scores.dtype == torch.float32 and
+                  scores.get_device() == dev and scores.is_contiguous())
+        if ok and q_start is not None:
+            ok = (q_start.shape == (S + 1,) and q_start.dtype == torch.int32 and q_start.get_device() == dev and
+                  q_start.is_contiguous())
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        extra = {} if scores is None else dict(scores=(scores, torch.float32, 3))
+        if q_start is not None:
+            extra["q_start"] = (q_start, torch.int32, 1)
+        _refuse(where, query=(query, None, 3), out=(out, None, 3), key_cache=(key_cache, None, 4),
+                value_cache=(value_cache, None, 4), block_tables=(block_tables, torch.int32, 2),
+                context_lens=(context_lens, torch.int32, 1), **extra,
+                workspace=(workspace, None, workspace.dim() if isinstance(workspace, torch.Tensor) else 1))
+    return dev, qs, ks, S
 
 
 def accumulate_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_context_len, partition_size=0) -> int:
@@ -315,22 +349,18 @@ def paged_attention_accumulate(out, scores, query, key_cache, value_cache, block
                                max_context_len, workspace, k_scale=None, v_scale=None, partition_size=0, stream=None):
     """paged_attention that also adds each cached token's attention weights, summed over the query heads of
     its kv head, to scores[S,Hkv,stride] (float32)."""
-    S, H, d = query.shape
-    NB, bs, Hkv, _ = key_cache.shape
-    _check_batch(out, scores, query, key_cache, value_cache, block_tables, context_lens)
-    if context_lens.shape[0] != S:
-        raise ValueError(f"context_lens: expected {S} lengths, got {context_lens.shape[0]}")
-    dev = _device(query, "query")
+    dev, (T, H, d), (NB, bs, Hkv, _), S = _batch("paged_attention_accumulate", out, scores, query, key_cache, value_cache,
+                                                 block_tables, context_lens, workspace)
+    if S != T:
+        raise ValueError(f"context_lens: expected {T} lengths, got {S}")
     ks, vs = _scale_operands(k_scale, v_scale, key_cache, dev)
     st = lib.pa_paged_attention_accumulate(
-        _operand(out, "out", None, 3, dev), _operand(scores, "scores", torch.float32, 3, dev), scores.shape[2],
-        _operand(query, "query", None, 3, dev), dtype_code(query.dtype), _operand(key_cache, "key_cache", None, 4, dev),
-        _operand(value_cache, "value_cache", None, 4, dev), cache_code(key_cache, k_scale), ks, vs,
-        _operand(block_tables, "block_tables", torch.int32, 2, dev), block_tables.shape[1],
-        _operand(context_lens, "context_lens", torch.int32, 1, dev), S, H, Hkv, d, bs, NB, int(max_context_len),
-        float(scale), int(partition_size), _operand(workspace, "workspace", None, workspace.dim(), dev),
-        workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "pa_paged_attention_accumulate")
+        out.data_ptr(), scores.data_ptr(), scores.shape[2], query.data_ptr(), dtype_code(query.dtype),
+        key_cache.data_ptr(), value_cache.data_ptr(), cache_code(key_cache, k_scale), ks, vs, block_tables.data_ptr(),
+        block_tables.shape[1], context_lens.data_ptr(), S, H, Hkv, d, bs, NB, int(max_context_len), float(scale),
+        int(partition_size), workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if st != PA_OK:
+        _check(st, "pa_paged_attention_accumulate")
     return out
 
 
@@ -354,11 +384,6 @@ def paged_prefill(out, query, key_cache, value_cache, block_tables, context_lens
     _check(st, "pa_paged_prefill")
 
 
-def _check_chunks(q_start, S):
-    if q_start.dim() != 1 or q_start.shape[0] != S + 1:
-        raise ValueError(f"q_start: expected {S + 1} entries, got shape {tuple(q_start.shape)}")
-
-
 def make_prefill_accumulate_workspace(num_q_tokens, num_heads, device="cuda") -> torch.Tensor:
     """A zeroed workspace for paged_prefill_accumulate of up to num_q_tokens query tokens."""
     n = lib.pa_paged_prefill_accumulate_workspace_size(num_q_tokens, num_heads)
@@ -371,23 +396,16 @@ def paged_prefill_accumulate(out, scores, query, key_cache, value_cache, block_t
                              max_q_len, max_context_len, workspace, window=0, k_scale=None, v_scale=None, stream=None):
     """paged_prefill that also adds the attention weights of each chunk's last `window` tokens (0: all of
     them), summed over the query heads of each kv head, to scores[S,Hkv,stride] (float32)."""
-    T, H, d = query.shape
-    NB, bs, Hkv, _ = key_cache.shape
-    S = context_lens.shape[0]
-    _check_batch(out, scores, query, key_cache, value_cache, block_tables, context_lens)
-    _check_chunks(q_start, S)
-    dev = _device(query, "query")
+    dev, (T, H, d), (NB, bs, Hkv, _), S = _batch("paged_prefill_accumulate", out, scores, query, key_cache, value_cache,
+                                                 block_tables, context_lens, workspace, q_start)
     ks, vs = _scale_operands(k_scale, v_scale, key_cache, dev)
     st = lib.pa_paged_prefill_accumulate(
-        _operand(out, "out", None, 3, dev), _operand(scores, "scores", torch.float32, 3, dev), scores.shape[2],
-        _operand(query, "query", None, 3, dev), dtype_code(query.dtype), _operand(key_cache, "key_cache", None, 4, dev),
-        _operand(value_cache, "value_cache", None, 4, dev), cache_code(key_cache, k_scale), ks, vs,
-        _operand(block_tables, "block_tables", torch.int32, 2, dev), block_tables.shape[1],
-        _operand(context_lens, "context_lens", torch.int32, 1, dev), _operand(q_start, "q_start", torch.int32, 1, dev),
-        S, T, H, Hkv, d, bs, NB, int(max_q_len), int(max_context_len), int(window), float(scale),
-        _operand(workspace, "workspace", None, workspace.dim(), dev), workspace.numel() * workspace.element_size(),
-        _stream(stream))
-    _check(st, "pa_paged_prefill_accumulate")
+        out.data_ptr(), scores.data_ptr(), scores.shape[2], query.data_ptr(), dtype_code(query.dtype),
+        key_cache.data_ptr(), value_cache.data_ptr(), cache_code(key_cache, k_scale), ks, vs, block_tables.data_ptr(),
+        block_tables.shape[1], context_lens.data_ptr(), q_start.data_ptr(), S, T, H, Hkv, d, bs, NB, int(max_q_len),
+        int(max_context_len), int(window), float(scale), workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if st != PA_OK:
+        _check(st, "pa_paged_prefill_accumulate")
     return out
 
 
@@ -405,22 +423,16 @@ def paged_cross_attention(out, query, key_cache, value_cache, block_tables, cont
                           max_context_len, workspace, k_scale=None, v_scale=None, stream=None):
     """Cross attention: rows q_start[s]..q_start[s+1]-1 of query[T,H,d] attend to all context_lens[s] cached
     states of sequence s's encoder (no causal mask; zeros where there are none)."""
-    T, H, d = query.shape
-    NB, bs, Hkv, _ = key_cache.shape
-    S = context_lens.shape[0]
-    _check_batch(out, None, query, key_cache, value_cache, block_tables, context_lens)
-    _check_chunks(q_start, S)
-    dev = _device(query, "query")
+    dev, (T, H, d), (NB, bs, Hkv, _), S = _batch("paged_cross_attention", out, None, query, key_cache, value_cache,
+                                                 block_tables, context_lens, workspace, q_start)
     ks, vs = _scale_operands(k_scale, v_scale, key_cache, dev)
     st = lib.pa_paged_cross_attention(
-        _operand(out, "out", None, 3, dev), _operand(query, "query", None, 3, dev), dtype_code(query.dtype),
-        _operand(key_cache, "key_cache", None, 4, dev), _operand(value_cache, "value_cache", None, 4, dev),
-        cache_code(key_cache, k_scale), ks, vs, _operand(block_tables, "block_tables", torch.int32, 2, dev),
-        block_tables.shape[1], _operand(context_lens, "context_lens", torch.int32, 1, dev),
-        _operand(q_start, "q_start", torch.int32, 1, dev), S, T, H, Hkv, d, bs, NB, int(max_q_len),
-        int(max_context_len), float(scale), _operand(workspace, "workspace", None, workspace.dim(), dev),
-        workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "pa_paged_cross_attention")
+        out.data_ptr(), query.data_ptr(), dtype_code(query.dtype), key_cache.data_ptr(), value_cache.data_ptr(),
+        cache_code(key_cache, k_scale), ks, vs, block_tables.data_ptr(), block_tables.shape[1],
+        context_lens.data_ptr(), q_start.data_ptr(), S, T, H, Hkv, d, bs, NB, int(max_q_len), int(max_context_len),
+        float(scale), workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if st != PA_OK:
+        _check(st, "pa_paged_cross_attention")
     return out
 
 
@@ -459,18 +471,22 @@ def reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, k_scale=
     _check(st, "pa_reshape_and_cache")
 
 
-def _token_rows(t, name, dtype, dev):
-    """Pointer and token stride of a [T, heads, d] tensor whose tokens are dense rows, possibly further
-    apart than a row (a slice of a fused projection)."""
-    T, H, d = t.shape
-    s0, s1, s2 = t.stride()
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
-    if (d > 1 and s2 != 1) or (H > 1 and s1 != d):
-        raise ValueError(f"{name}: each token's [heads, head_size] row must be dense, got strides {t.stride()}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: must be a CUDA tensor on the current device cuda:{dev}, got {t.device}")
-    return t.data_ptr(), (s0 if T > 1 else H * d)
+def _refuse_rows(dt, dev, **rows):
+    """Raises for the first [T, heads, d] operand whose tokens are not dense rows of dt on the device; such rows may
+    lie further apart than their width (slices of a fused projection)."""
+    for name, t in rows.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+        if t.dim() != 3 or t.dtype != dt:
+            raise ValueError(f"{name}: expected 3 dimensions of {dt}, got shape {tuple(t.shape)} {t.dtype}")
+        if not _dense_rows(t.shape, t.stride()):
+            raise ValueError(f"{name}: each token's [heads, head_size] row must be dense, got strides {t.stride()}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: must be a CUDA tensor on the current device cuda:{dev}, got {t.device}")
+
+
+def _dense_rows(shape, stride):
+    return (stride[2] == 1 or shape[2] == 1) and (stride[1] == shape[2] or shape[1] == 1)
 
 
 def rope_reshape_and_cache(query_out, query, key, value, key_cache, value_cache, slot_mapping, positions, inv_freq,
@@ -479,29 +495,43 @@ def rope_reshape_and_cache(query_out, query, key, value, key_cache, value_cache,
     several axes (positions[A,T] int32; inv_freq[R/2] float32; freq_axis[R/2] int32, the axis each
     frequency follows), and write value beside the keys. Token rows may be strided (slices of a fused
     projection); query_out may be query."""
-    T, H, d = query.shape
-    NB, bs, Hkv, d2 = key_cache.shape
-    _same(key_cache, value_cache, "key_cache/value_cache")
-    if query_out.shape != query.shape:
-        raise ValueError(f"query_out/query: shapes differ ({tuple(query_out.shape)} vs {tuple(query.shape)})")
-    if key.shape != (T, Hkv, d2) or value.shape != (T, Hkv, d2) or d2 != d:
-        raise ValueError(f"key/value: expected {(T, Hkv, d)}, got {tuple(key.shape)} and {tuple(value.shape)}")
-    if positions.dim() != 2 or positions.shape[1] != T or slot_mapping.shape != (T,):
-        raise ValueError(f"positions/slot_mapping: expected [axes, {T}] and [{T}], got {tuple(positions.shape)} and "
-                         f"{tuple(slot_mapping.shape)}")
-    if inv_freq.shape != freq_axis.shape:
-        raise ValueError(f"inv_freq/freq_axis: lengths differ ({tuple(inv_freq.shape)} vs {tuple(freq_axis.shape)})")
-    dev, dt = _device(query, "query"), query.dtype
-    ks, vs = _scale_operands(k_scale, v_scale, key_cache, dev)
+    try:
+        dev, qs, ks, dt, ct = query.get_device(), query.shape, key_cache.shape, query.dtype, key_cache.dtype
+        (T, H, d), (NB, bs, Hkv, _) = qs, ks
+        kv, half = key.shape, inv_freq.shape
+        so, sq, sk, sv = query_out.stride(), query.stride(), key.stride(), value.stride()
+        ok = (kv == (T, Hkv, d) and value.shape == kv and query_out.shape == qs and ks[3] == d and
+              value_cache.shape == ks and value_cache.dtype == ct and query_out.dtype == dt and key.dtype == dt and
+              value.dtype == dt and _dense_rows(qs, so) and _dense_rows(qs, sq) and _dense_rows(kv, sk) and
+              _dense_rows(kv, sv) and slot_mapping.shape == (T,) and slot_mapping.dtype == torch.int64 and
+              positions.dim() == 2 and positions.shape[1] == T and positions.dtype == torch.int32 and
+              len(half) == 1 and freq_axis.shape == half and inv_freq.dtype == torch.float32 and
+              freq_axis.dtype == torch.int32 and dev >= 0 and dev == torch._C._cuda_getDevice() and
+              query_out.get_device() == dev and key.get_device() == dev and value.get_device() == dev and
+              key_cache.get_device() == dev and value_cache.get_device() == dev and
+              slot_mapping.get_device() == dev and positions.get_device() == dev and inv_freq.get_device() == dev and
+              freq_axis.get_device() == dev and key_cache.is_contiguous() and value_cache.is_contiguous() and
+              slot_mapping.is_contiguous() and positions.is_contiguous() and inv_freq.is_contiguous() and
+              freq_axis.is_contiguous())
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        if isinstance(query, torch.Tensor):
+            _refuse_rows(query.dtype, _device(query, "query"), query=query, query_out=query_out, key=key, value=value)
+        _refuse("rope_reshape_and_cache", key_cache=(key_cache, None, 4), value_cache=(value_cache, None, 4),
+                slot_mapping=(slot_mapping, torch.int64, 1), positions=(positions, torch.int32, 2),
+                inv_freq=(inv_freq, torch.float32, 1), freq_axis=(freq_axis, torch.int32, 1), query=(query, None, 3),
+                query_out=(query_out, None, 3), key=(key, None, 3), value=(value, None, 3))
+    ksc, vsc = _scale_operands(k_scale, v_scale, key_cache, dev)
+    one = T <= 1  # a single token's stride says nothing
     st = lib.pa_rope_reshape_and_cache(
-        *_token_rows(query_out, "query_out", dt, dev), *_token_rows(query, "query", dt, dev),
-        *_token_rows(key, "key", dt, dev), *_token_rows(value, "value", dt, dev), dtype_code(dt),
-        _operand(key_cache, "key_cache", None, 4, dev), _operand(value_cache, "value_cache", None, 4, dev),
-        cache_code(key_cache, k_scale), ks, vs, _operand(slot_mapping, "slot_mapping", torch.int64, 1, dev),
-        _operand(positions, "positions", torch.int32, 2, dev), positions.shape[0],
-        _operand(inv_freq, "inv_freq", torch.float32, 1, dev), _operand(freq_axis, "freq_axis", torch.int32, 1, dev),
-        2 * inv_freq.shape[0], int(bool(interleaved)), T, H, Hkv, d, bs, NB, _stream(stream))
-    _check(st, "pa_rope_reshape_and_cache")
+        query_out.data_ptr(), H * d if one else so[0], query.data_ptr(), H * d if one else sq[0], key.data_ptr(),
+        Hkv * d if one else sk[0], value.data_ptr(), Hkv * d if one else sv[0], dtype_code(dt), key_cache.data_ptr(),
+        value_cache.data_ptr(), cache_code(key_cache, k_scale), ksc, vsc, slot_mapping.data_ptr(), positions.data_ptr(),
+        positions.shape[0], inv_freq.data_ptr(), freq_axis.data_ptr(), 2 * half[0], 1 if interleaved else 0, T, H, Hkv, d,
+        bs, NB, _stream(stream))
+    if st != PA_OK:
+        _check(st, "pa_rope_reshape_and_cache")
     return query_out
 
 
@@ -516,31 +546,39 @@ def evict_tokens(kept, new_lens, scores_out, scores, key_cache, value_cache, blo
     and the highest scores[S,Hkv,stride] between them stay, moved together in order into the blocks of
     dst_block_tables (block_tables itself: in place). Writes kept[S,Hkv,budget], new_lens[S] and
     scores_out. Per-block FP8 scales (a 2-D k_scale) are refused: their codes cannot change blocks."""
-    NB, bs, Hkv, d = key_cache.shape
-    S = context_lens.shape[0]
-    _same(key_cache, value_cache, "key_cache/value_cache")
-    _same(scores_out, scores, "scores_out/scores")
-    if scores.dim() != 3 or tuple(scores.shape[:2]) != (S, Hkv):
-        raise ValueError(f"scores: expected ({S}, {Hkv}, stride), got {tuple(scores.shape)}")
-    if tuple(kept.shape) != (S, Hkv, int(budget)) or tuple(new_lens.shape) != (S,):
-        raise ValueError(f"kept/new_lens: expected {(S, Hkv, int(budget))} and {(S,)}, got {tuple(kept.shape)} and "
-                         f"{tuple(new_lens.shape)}")
-    if block_tables.dim() != 2 or dst_block_tables.dim() != 2 or block_tables.shape[0] != S or \
-            dst_block_tables.shape[0] != S:
-        raise ValueError(f"block tables: expected {S} rows, got {tuple(block_tables.shape)} and "
-                         f"{tuple(dst_block_tables.shape)}")
-    dev, i32 = _device(scores, "scores"), torch.int32
+    i32 = torch.int32
+    try:
+        dev, ks, ss = scores.get_device(), key_cache.shape, scores.shape
+        (NB, bs, Hkv, d), (S,) = ks, context_lens.shape
+        ok = (len(ss) == 3 and ss[0] == S and ss[1] == Hkv and scores_out.shape == ss and value_cache.shape == ks and
+              value_cache.dtype == key_cache.dtype and kept.shape == (S, Hkv, budget) and new_lens.shape == (S,) and
+              block_tables.dim() == 2 and dst_block_tables.dim() == 2 and block_tables.shape[0] == S and
+              dst_block_tables.shape[0] == S and scores.dtype == torch.float32 and scores_out.dtype == torch.float32 and
+              kept.dtype == i32 and new_lens.dtype == i32 and block_tables.dtype == i32 and
+              dst_block_tables.dtype == i32 and context_lens.dtype == i32 and dev >= 0 and
+              dev == torch._C._cuda_getDevice() and kept.get_device() == dev and new_lens.get_device() == dev and
+              scores_out.get_device() == dev and key_cache.get_device() == dev and value_cache.get_device() == dev and
+              block_tables.get_device() == dev and dst_block_tables.get_device() == dev and
+              context_lens.get_device() == dev and workspace.get_device() == dev and kept.is_contiguous() and
+              new_lens.is_contiguous() and scores.is_contiguous() and scores_out.is_contiguous() and
+              key_cache.is_contiguous() and value_cache.is_contiguous() and block_tables.is_contiguous() and
+              dst_block_tables.is_contiguous() and context_lens.is_contiguous() and workspace.is_contiguous())
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _refuse("evict_tokens", scores=(scores, torch.float32, 3), scores_out=(scores_out, torch.float32, 3),
+                kept=(kept, i32, 3), new_lens=(new_lens, i32, 1), key_cache=(key_cache, None, 4),
+                value_cache=(value_cache, None, 4), block_tables=(block_tables, i32, 2),
+                dst_block_tables=(dst_block_tables, i32, 2), context_lens=(context_lens, i32, 1),
+                workspace=(workspace, None, workspace.dim() if isinstance(workspace, torch.Tensor) else 1))
     st = lib.pa_evict_tokens(
-        _operand(kept, "kept", i32, 3, dev), _operand(new_lens, "new_lens", i32, 1, dev),
-        _operand(scores_out, "scores_out", torch.float32, 3, dev), _operand(scores, "scores", torch.float32, 3, dev),
-        scores.shape[2], _operand(key_cache, "key_cache", None, 4, dev),
-        _operand(value_cache, "value_cache", None, 4, dev), cache_code(key_cache, k_scale),
-        _operand(block_tables, "block_tables", i32, 2, dev), block_tables.shape[1],
-        _operand(dst_block_tables, "dst_block_tables", i32, 2, dev), dst_block_tables.shape[1],
-        _operand(context_lens, "context_lens", i32, 1, dev), S, Hkv, d, bs, NB, int(max_context_len), int(budget),
-        int(num_sink), int(num_recent), _operand(workspace, "workspace", None, workspace.dim(), dev),
-        workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "pa_evict_tokens")
+        kept.data_ptr(), new_lens.data_ptr(), scores_out.data_ptr(), scores.data_ptr(), ss[2], key_cache.data_ptr(),
+        value_cache.data_ptr(), cache_code(key_cache, k_scale), block_tables.data_ptr(), block_tables.shape[1],
+        dst_block_tables.data_ptr(), dst_block_tables.shape[1], context_lens.data_ptr(), S, Hkv, d, bs, NB,
+        int(max_context_len), int(budget), int(num_sink), int(num_recent), workspace.data_ptr(), workspace.nbytes,
+        _stream(stream))
+    if st != PA_OK:
+        _check(st, "pa_evict_tokens")
 
 
 def copy_blocks(key_cache, value_cache, block_mapping, stream=None):
