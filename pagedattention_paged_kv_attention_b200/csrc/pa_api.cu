@@ -267,15 +267,6 @@ AccumulateLayout accumulate_layout(size_t base, int num_seqs, int num_heads, int
   return w;
 }
 
-template <int U>
-cudaError_t launch_weights(const pa::AttnArgs& a, float* scores, int score_stride, int max_context_len,
-                           cudaStream_t st) {
-  const unsigned chunks = static_cast<unsigned>(ceil_div(max_context_len, pa::kWeightTokens));
-  const unsigned heads = static_cast<unsigned>(a.num_kv_heads), seqs = static_cast<unsigned>(a.num_seqs);
-  return pa_host::launch_overlapped(pa::attention_weights_kernel<U>, dim3(chunks, heads, seqs),
-                                    dim3(pa::kWeightThreads), 0, st, a, scores, static_cast<long long>(score_stride));
-}
-
 }  // namespace
 
 namespace pa_host {
@@ -426,7 +417,11 @@ pa_status pa_paged_attention_accumulate(void* out, float* scores, int score_stri
   if (!scores || !aligned(scores, 4)) return PA_ERR_INVALID_ARGUMENT;
   if (!workspace || !aligned(workspace, 16)) return PA_ERR_INVALID_ARGUMENT;
   const AccumulateLayout w = accumulate_layout(plan.ws.total, num_seqs, num_heads, max_context_len, plan.partitions);
-  if (w.total == 0 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  // The finish kernel's grid: a CTA per row at most, and one per chunk of a kv head's tokens.
+  const long long finish_blocks =
+      static_cast<long long>(ceil_div(max_context_len, pa::kWeightTokens)) * num_kv_heads * num_seqs +
+      static_cast<long long>(num_seqs) * num_heads;
+  if (w.total == 0 || finish_blocks > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
   if (workspace_bytes < w.total) return PA_ERR_WORKSPACE_TOO_SMALL;
 
   AttnLaunch l;
@@ -442,15 +437,9 @@ pa_status pa_paged_attention_accumulate(void* out, float* scores, int score_stri
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = bf16 ? pa::launch_accumulate_bf16(l.tk, l.tv, l.a, fp8, head_size, plan.g_tile, l.grid, st)
                        : pa::launch_accumulate_f16(l.tk, l.tv, l.a, fp8, head_size, plan.g_tile, l.grid, st);
-  if (e == cudaSuccess && plan.partitions > 1)
-    e = bf16 ? pa::launch_reduce_bf16(l.a, head_size, st) : pa::launch_reduce_f16(l.a, head_size, st);
-  if (e == cudaSuccess && max_context_len > 0) {
-    const int group = num_heads / num_kv_heads;
-    e = group == 1   ? launch_weights<1>(l.a, scores, score_stride, max_context_len, st)
-        : group == 2 ? launch_weights<2>(l.a, scores, score_stride, max_context_len, st)
-        : group <= 4 ? launch_weights<4>(l.a, scores, score_stride, max_context_len, st)
-                     : launch_weights<8>(l.a, scores, score_stride, max_context_len, st);
-  }
+  if (e == cudaSuccess && max_context_len > 0)
+    e = bf16 ? pa::launch_finish_bf16(l.a, head_size, scores, score_stride, max_context_len, st)
+             : pa::launch_finish_f16(l.a, head_size, scores, score_stride, max_context_len, st);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -488,7 +488,15 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
   }
 #endif
   OrderTable* order = reinterpret_cast<OrderTable*>(smem + Lay::kOrder);
-  if (warp == 0) build_order(order, args, lane);
+  // With an item at most for every CTA, CTA i takes item i: no order, and no tickets, whose chains of loads are
+  // most of a small call's time. (The plain mode is left as it was.)
+  const bool one_each = MODE != kDecode && args.num_items <= gridDim.x;
+  if (warp == 0) {
+    if (!one_each)
+      build_order(order, args, lane);
+    else if (lane == 0)
+      order->ok = 0;
+  }
   __syncthreads();
 
   if (warp == 0) {
@@ -542,7 +550,7 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
 #define PA_CLAIM_STEP()                                                                                \
   do {                                                                                                 \
     if (claim_step == 0) {                                                                             \
-      if (lane == 0) pend_t = atomicAdd(args.header + kWsWork, 1u);                                    \
+      if (lane == 0) pend_t = one_each ? num_tickets : atomicAdd(args.header + kWsWork, 1u);           \
     } else if (claim_step == 1) {                                                                      \
       nxt_idx = __shfl_sync(0xffffffffu, pend_t, 0);                                                   \
       if (nxt_idx < num_tickets) {                                                                     \
@@ -570,7 +578,7 @@ paged_attention_main(const __grid_constant__ CUtensorMap tmap_k, const __grid_co
 
     {
       unsigned int t0 = 0;
-      if (lane == 0) t0 = atomicAdd(args.header + kWsWork, 1u);
+      if (lane == 0) t0 = one_each ? blockIdx.x : atomicAdd(args.header + kWsWork, 1u);
       cur_idx = __shfl_sync(0xffffffffu, t0, 0);
       PA_PREPARE(cur_idx, cur_c, cur_L, cur_ids);
     }
@@ -1280,23 +1288,11 @@ __device__ __forceinline__ void merge_range(const AttnArgs& a, size_t base, int 
 // MAXP (SPLIT = false): a bound on the partition count the launch was sized for (4, 8 or 16), so that a
 // row's preloaded values take no more registers than it needs and more warps stay resident.
 // ROWS: the row of out is found through q_start (kDecodeRows).
-template <typename QT, int D, bool SPLIT, int MAXP = kReduceSplitAbove, bool ROWS = false>
-__global__ void __launch_bounds__(kReduceWarps * 32)
-paged_attention_reduce(const AttnArgs args) {
+template <typename QT, int D, bool SPLIT, int MAXP, bool ROWS>
+__device__ __forceinline__ void reduce_rows(const AttnArgs& args, unsigned int block) {
   constexpr int kPer = D / 32;  // elements per lane: 4 for d = 128, 2 for d = 64
-  grid_dependency_wait();
-  grid_dependents_launch();
-#ifdef PA_TRACE
-  if (threadIdx.x == 0) atomicMax(args.trace, ~global_timer_ns());
-  struct TraceEnd {
-    unsigned long long* t;
-    __device__ ~TraceEnd() {  // thread 0's exit stands for its CTA's
-      if (threadIdx.x == 0) atomicMax(t + 1, global_timer_ns());
-    }
-  } trace_end{args.trace};
-#endif
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long row = SPLIT ? static_cast<long>(blockIdx.x) : static_cast<long>(blockIdx.x) * kReduceWarps + warp;
+  const long row = SPLIT ? static_cast<long>(block) : static_cast<long>(block) * kReduceWarps + warp;
   if (row >= static_cast<long>(args.num_seqs) * args.num_heads) return;
   const int s = static_cast<int>(row / args.num_heads);
   const int L = args.context_lens[s];
@@ -1430,6 +1426,23 @@ paged_attention_reduce(const AttnArgs args) {
   } else {
     *reinterpret_cast<uint32_t*>(out) = pack2<QT>(acc[0] * r, acc[1] * r);
   }
+}
+
+template <typename QT, int D, bool SPLIT, int MAXP = kReduceSplitAbove, bool ROWS = false>
+__global__ void __launch_bounds__(kReduceWarps * 32)
+paged_attention_reduce(const AttnArgs args) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+#ifdef PA_TRACE
+  if (threadIdx.x == 0) atomicMax(args.trace, ~global_timer_ns());
+  struct TraceEnd {
+    unsigned long long* t;
+    __device__ ~TraceEnd() {  // thread 0's exit stands for its CTA's
+      if (threadIdx.x == 0) atomicMax(t + 1, global_timer_ns());
+    }
+  } trace_end{args.trace};
+#endif
+  reduce_rows<QT, D, SPLIT, MAXP, ROWS>(args, blockIdx.x);
 }
 
 }  // namespace pa

@@ -7,7 +7,4 @@ cudaError_t launch_attention_bf16(const CUtensorMap& tk, const CUtensorMap& tv, 
   if (fp8_cache) return launch_attention<__nv_bfloat16, __nv_fp8_e4m3>(tk, tv, a, D, G, grid, stream);
   return launch_attention<__nv_bfloat16, __nv_bfloat16>(tk, tv, a, D, G, grid, stream);
 }
-cudaError_t launch_reduce_bf16(const AttnArgs& a, int D, cudaStream_t stream) {
-  return D == 128 ? launch_reduce<__nv_bfloat16, 128>(a, stream) : launch_reduce<__nv_bfloat16, 64>(a, stream);
-}
 }  // namespace pa

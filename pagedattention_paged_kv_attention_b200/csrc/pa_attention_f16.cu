@@ -7,7 +7,4 @@ cudaError_t launch_attention_f16(const CUtensorMap& tk, const CUtensorMap& tv, c
   if (fp8_cache) return launch_attention<__half, __nv_fp8_e4m3>(tk, tv, a, D, G, grid, stream);
   return launch_attention<__half, __half>(tk, tv, a, D, G, grid, stream);
 }
-cudaError_t launch_reduce_f16(const AttnArgs& a, int D, cudaStream_t stream) {
-  return D == 128 ? launch_reduce<__half, 128>(a, stream) : launch_reduce<__half, 64>(a, stream);
-}
 }  // namespace pa

@@ -28,7 +28,7 @@ cudaError_t launch_reduce(const AttnArgs& a, cudaStream_t stream) {
                                     stream, a);
 }
 
-// kDecodeWeights: the caller launches the merge and the weights kernel.
+// kDecodeWeights: the caller launches the kernel that merges and forms the weights.
 template <typename QT, typename KVT, int D, int G, bool BS = false, int MODE = kDecode>
 cudaError_t launch_attention_one(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, int grid,
                                  cudaStream_t stream) {
@@ -92,10 +92,12 @@ cudaError_t launch_attention_bf16(const CUtensorMap& tk, const CUtensorMap& tv, 
 cudaError_t launch_attention_f16(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, bool fp8_cache,
                                  int D, int G, int grid, cudaStream_t stream);
 
-// The merge alone (defined beside them), and the launches of the other modes (pa_rows_<dtype>.cu,
-// pa_accumulate_<dtype>.cu).
-cudaError_t launch_reduce_bf16(const AttnArgs& a, int D, cudaStream_t stream);
-cudaError_t launch_reduce_f16(const AttnArgs& a, int D, cudaStream_t stream);
+// The launches of the other modes (pa_rows_<dtype>.cu, pa_accumulate_<dtype>.cu), and the kernel that follows the
+// weight-scoring one: the merge and the weights.
+cudaError_t launch_finish_bf16(const AttnArgs& a, int D, float* scores, long long score_stride, int max_context_len,
+                               cudaStream_t stream);
+cudaError_t launch_finish_f16(const AttnArgs& a, int D, float* scores, long long score_stride, int max_context_len,
+                              cudaStream_t stream);
 cudaError_t launch_rows_bf16(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, bool fp8_cache, int D,
                              int G, int grid, cudaStream_t stream);
 cudaError_t launch_rows_f16(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, bool fp8_cache, int D,

@@ -4,7 +4,7 @@
 //   scores[s][kvh][t] += sum_g 2^(z_gt - lse_g),   lse_g = m_g + log2 sum_t 2^(z_gt - m_g),
 // over the query heads g of the kv head; z is the scaled score in log2 units. One decode step's z (every
 // token of every head) and the softmax statistics of each context partition come from
-// paged_attention_main's W instantiations; this kernel joins the partitions' statistics and sums the
+// paged_attention_main's kDecodeWeights instantiations; the finish kernel joins the partitions' statistics and sums the
 // heads' weights. A thread owns its tokens' scores and adds the heads in order, so results do not depend
 // on timing.
 #pragma once
@@ -20,17 +20,15 @@ constexpr int kWeightRound = 4 * kWeightThreads;   // tokens of a CTA's round, 4
 constexpr int kWeightTokens = 4 * kWeightRound;    // tokens of one CTA
 constexpr int kWeightHeads = 64;                   // query heads whose statistics are joined at a time
 
-// grid (token chunks, kv heads, sequences). U: heads whose scores a thread has in flight. The first ones' scores and
-// sums are fetched beside the statistics, so a CTA's first round costs one chain of loads.
+// U: heads whose scores a thread has in flight. The first ones' scores and sums are fetched beside the statistics,
+// so a CTA's first round costs one chain of loads.
 template <int U>
-__global__ void __launch_bounds__(kWeightThreads)
-attention_weights_kernel(const AttnArgs a, float* __restrict__ scores, long long score_stride) {
+__device__ __forceinline__ void weight_tokens(const AttnArgs& a, float* __restrict__ scores, long long score_stride,
+                                              unsigned int chunk, int kvh, int s) {
   __shared__ float lse[kWeightHeads];
-  grid_dependency_wait();
-  grid_dependents_launch();
-  const int s = blockIdx.z, kvh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int L = a.context_lens[s];
-  const long long t0 = static_cast<long long>(blockIdx.x) * kWeightTokens;
+  const long long t0 = static_cast<long long>(chunk) * kWeightTokens;
   if (L <= 0 || context_len_invalid(L, a) || t0 >= L) return;
   const int left = static_cast<int>(min(static_cast<long long>(kWeightTokens), L - t0));
   const int n_parts = (L - 1) / a.partition_size + 1;
@@ -90,6 +88,26 @@ attention_weights_kernel(const AttnArgs a, float* __restrict__ scores, long long
         if (t + k < left) out[t + k] = old[k] + acc[k];
     }
   }
+}
+
+// What is left after the main kernel: the merge of the partitions (its first reduce_blocks CTAs; none with one
+// partition) and the weights, side by side as neither needs the other.
+template <typename QT, int D, bool SPLIT, int MAXP, int U>
+__global__ void __launch_bounds__(kWeightThreads)
+attention_finish_kernel(const AttnArgs a, float* scores, long long score_stride, unsigned int chunks,
+                        unsigned int reduce_blocks) {
+  static_assert(kWeightThreads == kReduceWarps * 32, "one block shape for both");
+  grid_dependency_wait();
+  grid_dependents_launch();
+  if (blockIdx.x < reduce_blocks) {
+    reduce_rows<QT, D, SPLIT, MAXP, false>(a, blockIdx.x);
+    return;
+  }
+  unsigned int i = blockIdx.x - reduce_blocks;
+  const unsigned int chunk = i % chunks;
+  i /= chunks;
+  weight_tokens<U>(a, scores, score_stride, chunk, static_cast<int>(i % a.num_kv_heads),
+                   static_cast<int>(i / a.num_kv_heads));
 }
 
 }  // namespace pa
