@@ -23,10 +23,10 @@
  *    aligned. Tensors are dense, row-major, in the layouts given below.
  *  - Asynchrony: each call validates its arguments on the host, enqueues its kernels on `stream` and
  *    returns without synchronising ([T] sec. 3.2). A NULL stream is the legacy default stream. The
- *    kernels of pa_copy_blocks, pa_reshape_and_cache and pa_paged_attention(_static) are launched with
- *    programmatic stream serialisation: one may be scheduled while the previous kernel in the stream
- *    finishes, but it waits for that kernel's completion and memory before its first global access,
- *    so every memory effect keeps stream order.
+ *    kernels of pa_copy_blocks, pa_reshape_and_cache, pa_rope_reshape_and_cache, pa_evict_tokens and
+ *    pa_paged_attention(_static, _accumulate) are launched with programmatic stream serialisation: one
+ *    may be scheduled while the previous kernel in the stream finishes, but it waits for that kernel's
+ *    completion and memory before its first global access, so every memory effect keeps stream order.
  *  - Errors: invalid arguments are reported before anything is enqueued (nothing runs, no CUDA call is
  *    made). Launch failures return PA_ERR_CUDA. The library never aborts, never throws across the ABI
  *    and its kernels never trap; contract violations that only the device can see (a block id
@@ -151,9 +151,10 @@ PA_API pa_status pa_paged_attention(void* out, const void* query, pa_dtype q_dty
                              void* workspace, size_t workspace_bytes, pa_stream_t stream);
 
 /*
- * Workspace bytes of pa_paged_attention_accumulate: pa_paged_attention_workspace_size(...) at its partition size, plus the scaled
- * scores of the step, 4 * num_seqs * num_heads * round_up(max_context_len, 64) bytes, and softmax statistics
- * of 8 bytes per (sequence, head, partition). Returns 0 if the arguments are invalid. Makes no CUDA call.
+ * Workspace bytes of pa_paged_attention_accumulate: pa_paged_attention_workspace_size(...) at its partition
+ * size, plus the scaled scores of the step, 4 * num_seqs * num_heads * round_up(max_context_len, 64) bytes,
+ * and softmax statistics of 8 bytes per (sequence, head, partition). Returns 0 if the arguments are invalid.
+ * Makes no CUDA call.
  */
 PA_API size_t pa_paged_attention_accumulate_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
                                                            int head_size, int max_context_len, int partition_size);
@@ -440,11 +441,11 @@ PA_API pa_status pa_copy_blocks_layers(void* const* key_caches, void* const* val
  *  key_cache,
  *  value_cache    [num_blocks][block_size][num_kv_heads][head_size]; read and written.
  *  block_tables   [num_seqs][max_blocks_per_seq] int32, the blocks that hold the tokens now.
- *  dst_block_tables [num_seqs][max_dst_blocks_per_seq] int32, the blocks that hold them afterwards (the
- *                 first ceil(min(L, budget) / block_size) entries are read). Entry i may be the sequence's
- *                 own block_tables entry i (compaction in place; block_tables may be passed itself) if
- *                 no other sequence reads that block; any other destination must be a block that no
- *                 sequence of the call reads. Destinations of one call are distinct.
+ *  dst_block_tables [num_seqs][max_dst_blocks_per_seq] int32, the blocks that hold them afterwards
+ *                 (pa_bm_plan_evict gives both tables). The first ceil(min(L, budget) / block_size) entries
+ *                 are read. Entry i may be the sequence's own block_tables entry i (compaction in place;
+ *                 block_tables may be passed itself) if no other sequence reads that block; any other
+ *                 destination must be a block that no sequence of the call reads. Destinations of one call are distinct.
  *  budget >= 1, num_sink >= 0, num_recent >= 0, num_sink + num_recent <= budget;
  *  max_dst_blocks_per_seq * block_size >= min(budget, max_context_len).
  *  workspace      >= PA_WORKSPACE_HEADER_BYTES, zeroed once; its first word is the device error word.

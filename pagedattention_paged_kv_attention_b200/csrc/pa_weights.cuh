@@ -3,10 +3,11 @@
 // A token's score is the sum of the softmax weights that queries have given it, per kv head:
 //   scores[s][kvh][t] += sum_g 2^(z_gt - lse_g),   lse_g = m_g + log2 sum_t 2^(z_gt - m_g),
 // over the query heads g of the kv head; z is the scaled score in log2 units. One decode step's z (every
-// token of every head) and the softmax statistics of each context partition come from
-// paged_attention_main's kDecodeWeights instantiations; the finish kernel joins the partitions' statistics and sums the
-// heads' weights. A thread owns its tokens' scores and adds the heads in order, so results do not depend
-// on timing.
+// token of every head) and the softmax statistics of each context partition come from paged_attention_main's
+// kDecodeWeights instantiations; the finish kernel joins the partitions' statistics and sums the heads' weights.
+// A thread owns its tokens' scores and adds the heads in order, so results do not depend on timing. Bound by the
+// scores' bytes, 4 written and 4 read per token and query head: profiled alone, 64 sequences of up to 1996 tokens,
+// 32/32 heads, 14 us beside a main kernel of 210; 128 of up to 4092, 64/8 heads, 29 beside 206.
 #pragma once
 
 #include <math.h>
