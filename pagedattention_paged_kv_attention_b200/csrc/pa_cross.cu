@@ -74,7 +74,7 @@ pa_status pa_paged_cross_attention(void* out, const void* query, pa_dtype q_dtyp
       context_lens, q_start, num_seqs, num_q_tokens, num_heads, num_kv_heads, head_size, block_size, num_blocks,
       max_q_len, scale, workspace, workspace_bytes, need, &empty);
   if (checked != PA_OK || empty) return checked;
-  // Single tokens are bound by the states' bytes: the decode kernel reads them at 90% of the copy bandwidth, a
+  // Single tokens are bound by the states' bytes: the decode kernel reads them at 82% of the copy bandwidth, a
   // tile of 128 query rows with few of them used at half (32 sequences, 8 kv heads, up to 6404 states: 87 and
   // 135 us).
   if (max_q_len == 1 && pa_host::decode_rows_supported(block_size, num_blocks))
