@@ -117,3 +117,30 @@ def test_two_graphs_share_workspaces(P):
         for a, b in zip(eager, graphed):
             same(a, b)
     assert all(P.get_device_error(w) == 0 for w in ws)
+
+
+LONE = [  # context lengths, chunk, query heads, kv heads, head size, cache
+    ([129, 256, 257, 384, 385, 128, 1], 5, 4, 4, 128, "16"),       # 2, 2, 3, 3, 4 key tiles; 1 and 1: one warpgroup
+    ([1000, 1, 640, 511, 1153, 2048, 2049], 128, 4, 4, 128, "16"),
+    ([1000, 130, 640, 511, 0, 2048, 700], 33, 8, 2, 64, "16"),
+    ([900, 129, 640, 255, 1153], 9, 16, 2, 128, "fp8"),
+    ([900, 129, 640, 257, 1153], 17, 4, 4, 128, "fp8_block"),
+    ([1500, 3, 5000], 7, 2, 1, 128, "16"),                         # keys shared by several CTAs as well
+]
+
+
+@pytest.mark.parametrize("case", LONE, ids=lambda c: "L%s_n%d_H%d_%d_d%d_%s" % ("-".join(map(str, c[0])), *c[1:]))
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_cross_attention_of_lone_query_tiles(P, case, dtype):
+    import test_gpu_cross as X
+    lens, n, H, Hkv, d, cache = case
+    chunks = [n] * len(lens)
+    st = X.make(lens, chunks, H, Hkv, d, 16, seed=sum(lens), cache=cache, dtype=dtype)
+    out = torch.full_like(st["q"], float("nan"))
+    ws = X.call(P, st, out)
+    torch.cuda.synchronize()
+    assert P.get_device_error(ws) == 0
+    X.check(st, out)
+    again = torch.empty_like(out)
+    X.call(P, st, again, ws=ws)
+    assert torch.equal(out, again)
