@@ -135,11 +135,6 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// The same without the ordering of memory accesses.
-__device__ __forceinline__ void cluster_barrier_relaxed() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-
 // The word at this address in the shared memory of the cluster's CTA `rank`.
 template <typename T>
 __device__ __forceinline__ T cluster_load(const T* p, int rank) {

@@ -77,7 +77,8 @@ extern "C" pa_status pa_evict_tokens(int32_t* kept, int32_t* new_lens, float* sc
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const unsigned heads = static_cast<unsigned>(num_kv_heads), seqs = static_cast<unsigned>(num_seqs);
   // As many CTAs a row as the GPU holds at once, so that no row waits for another's CTAs (16 rows of 16384 tokens
-  // x 8 heads, cut to 2048: 4 CTAs 66 us, 2 CTAs 86 us, 8 CTAs, two waves, 79 us), but none without a share.
+  // x 8 heads, cut to 2048, into other blocks and in place: 4 CTAs 69 and 68 us, 2 CTAs 78 and 91, 8 CTAs, two waves,
+  // 79 and 82), but none without a share.
   const int64_t fit = static_cast<int64_t>(sms) * pa::kEvictPerSm / (static_cast<int64_t>(heads) * seqs);
   const int64_t share = pa_host::ceil_div(max_context_len, pa::kEvictShare);
   const unsigned cluster = static_cast<unsigned>(

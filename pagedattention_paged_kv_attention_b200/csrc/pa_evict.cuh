@@ -15,9 +15,11 @@
 // would serialise a warp's atomics; the CTAs' counts are added through distributed shared memory.
 // Move: bound by HBM, every kept row is read and written once. A kept token never moves up (kept[j] >= j), so
 // walking j upwards, a round of rows read before any of them is written, may write over the very blocks that
-// are read: a slot is written after the rows that come from it were read.
-// 16 rows of 4096 to 16384 tokens x 8 heads of 128 (16-bit), cut to 2048: 66.5 us, 4.26 TB/s; selection and move in
-// kernels of their own took 79 us.
+// are read: a slot is written after the rows that come from it were read. Where a destination block is one of
+// the sequence's own, the cluster's barrier orders each round's reads before its writes (release and acquire: a
+// barrier without them does not wait for loads in flight); rows that go to other blocks need no order.
+// 16 rows of 4096 to 16384 tokens x 8 heads of 128 (16-bit), cut to 2048: 68.6 us into other blocks, 4.12 TB/s, 67.9
+// in place; one of 16384 tokens 19.2 and 22.2. Selection and move in kernels of their own took 79 us.
 #pragma once
 
 #include <math.h>
@@ -318,9 +320,8 @@ __device__ __forceinline__ void evict_select(EvictShared& sh, const EvictArgs& a
 }
 
 // grid (cluster, kv heads, sequences). In the move a strip is 16 << log_lanes bytes of the head's key or value
-// row, and a step is one strip of a round, kMoveUnroll loads of 32 >> log_lanes rows a warp and CTA. The cluster's
-// barrier parts a step's reads from its writes; the next step's rows are loaded before it (a slot is never
-// written before its row has been read, so reading early is safe). The scores move with the rows.
+// row, and a step is one strip of a round, kMoveUnroll loads of 32 >> log_lanes rows a warp and CTA. The scores
+// move with the rows.
 __global__ void __launch_bounds__(kEvictThreads, kEvictPerSm)
 evict_kernel(const EvictArgs a) {
   __shared__ EvictShared sh;
@@ -341,21 +342,25 @@ evict_kernel(const EvictArgs a) {
   }
   const float* w = a.scores + rowi * a.score_stride;
   float* wo = a.scores_out + rowi * a.score_stride;
-  const int n = min(L, a.budget);
+  const int n = min(L, a.budget), bs = a.block_size, blocks = n > 0 ? (n - 1) / bs + 1 : 0;
+  const int32_t* src = a.block_tables + static_cast<size_t>(s) * a.max_blocks_per_seq;
+  const int32_t* dst = a.dst_tables + static_cast<size_t>(s) * a.max_dst_blocks_per_seq;
+  const int from0 = tid < blocks ? src[tid] : 0, to0 = tid < blocks ? dst[tid] : -1;  // compared after the selection
   if (L <= a.budget) {
     for (int j = rank * kEvictThreads + tid; j < n; j += ctas * kEvictThreads) kept[j] = j;
   } else {
     evict_select(sh, a, L, rank, ctas, w, kept);
   }
   evict_sync(ctas);  // kept is complete; nothing reads this CTA's shared memory any more
-
   const int strips = (a.row_bytes + (16 << a.log_lanes) - 1) / (16 << a.log_lanes);
   const int rows = 32 >> a.log_lanes;                        // of one load
   const int log_round = kMoveLogLoads + 5 - a.log_lanes, round = 1 << log_round;  // rows of this CTA and round
-  const int32_t* src = a.block_tables + static_cast<size_t>(s) * a.max_blocks_per_seq;
-  const int32_t* dst = a.dst_tables + static_cast<size_t>(s) * a.max_dst_blocks_per_seq;
   const size_t token_bytes = static_cast<size_t>(a.num_kv_heads) * a.row_bytes;
-  const int bs = a.block_size, log_bs = a.log_block;
+  const int log_bs = a.log_block;
+  // Whether a slot that is written may be one that is read: every CTA of the cluster finds the same.
+  bool same_block = from0 == to0;
+  for (int i = tid + kEvictThreads; i < blocks; i += kEvictThreads) same_block = same_block || src[i] == dst[i];
+  const bool over = __syncthreads_or(same_block);
   auto in_block = [&](int t) { return log_bs >= 0 ? t >> log_bs : t / bs; };
   const int row0 = warp * (kMoveUnroll * rows) + (lane >> a.log_lanes);
   const int lane_col = (lane & ((1 << a.log_lanes) - 1)) * 16;
@@ -382,8 +387,9 @@ evict_kernel(const EvictArgs a) {
       }
       sh.slots[i] = f;
     }
-    __syncthreads();
-    // Step = (round, strip); the loads run one step ahead of the stores, each with a cursor of its own.
+    evict_sync(wo == w ? ctas : 1);  // in place, every CTA has read the stage's scores, which are now written over
+    // Step = (round, strip); loads and stores have a cursor each, and go two steps at a time (keys and values are an
+    // even number). A later round's rows come from slots above this round's.
     struct Cursor {
       int round, strip;
       const uint32_t* from;
@@ -420,28 +426,15 @@ evict_kernel(const EvictArgs a) {
       }
       next(c);
     };
-    // Waits until this lane's rows of a step have arrived, then for the cluster: the barrier itself orders
-    // no memory (one that does would wait for the stores before it as well).
-    auto all_read = [&](uint4 (&x)[kMoveUnroll]) {
-#pragma unroll
-      for (int i = 0; i < kMoveUnroll; ++i) asm volatile("" : "+r"(x[i].x), "+r"(x[i].y), "+r"(x[i].z), "+r"(x[i].w));
-      if (ctas > 1)
-        cluster_barrier_relaxed();
-      else
-        __syncthreads();
-    };
     uint4 x0[kMoveUnroll], x1[kMoveUnroll];
     Cursor in{0, 0, sh.slots + row0}, out = in;
-    load(x0, in);
-    while (out.round < rounds) {  // an even number of steps: keys and values
-      load(x1, in);
-      all_read(x0);
-      store(x0, out);
+    while (out.round < rounds) {
       load(x0, in);
-      all_read(x1);
+      load(x1, in);
+      if (over) evict_sync(ctas);
+      store(x0, out);
       store(x1, out);
     }
-    // Every CTA has read the stage's scores before the first barrier above.
     for (int i = tid; i < rounds * round; i += kEvictThreads) {
       const int j = lo + (((i >> log_round) * ctas + rank) << log_round) + (i & (round - 1));
       if (j < n) wo[j] = sh.score[i];
