@@ -23,6 +23,7 @@
 #pragma once
 
 #include <math.h>
+#include <stddef.h>
 
 #include "pa_device.cuh"
 
@@ -76,7 +77,7 @@ __device__ __forceinline__ uint32_t score_key(float w) {
 // next thread's, so that 16-byte reads of a warp do not meet in a bank.
 __device__ __forceinline__ int key_slot(int i) { return i + i / kEvictPer * 4; }
 
-struct EvictShared {
+struct alignas(16) EvictShared {
   union {
     struct {
       int hist[256 * kHistCopies];                // [digit][lane % kHistCopies]
@@ -91,10 +92,12 @@ struct EvictShared {
   uint32_t few[kEvictFew];
   int num_few, cta_sum[2];
   uint32_t all_few[kEvictFew];
-  int warp_sum[kEvictWarps][2];
+  int warp_sum[kEvictWarps];           // of two counts, 16 bits each, in a scan
   uint32_t prefix;
   int need, count;
 };
+static_assert(alignof(EvictShared) % 16 == 0 && offsetof(EvictShared, keys) % 16 == 0 && (kEvictPer + 4) % 4 == 0,
+              "keys are read 16 bytes at a time");
 
 // Keys of tokens that are not ranked: past the row, or kept whatever their score.
 constexpr uint32_t kKeyOut = 0u, kKeyEnd = 0xffffffffu;  // no score's key is either
@@ -117,12 +120,12 @@ __device__ __forceinline__ int2 evict_scan(EvictShared& sh, int x, int y, int2* 
     if (lane >= o) v += u;
   }
   __syncthreads();                     // the last scan's sums have been read
-  if (lane == 31) sh.warp_sum[warp][0] = v;
+  if (lane == 31) sh.warp_sum[warp] = v;
   __syncthreads();
   int all = 0, before = v - own;
 #pragma unroll
   for (int i = 0; i < kEvictWarps; ++i) {
-    const int c = sh.warp_sum[i][0];
+    const int c = sh.warp_sum[i];
     before += i < warp ? c : 0;
     all += c;
   }
@@ -216,10 +219,10 @@ __device__ __forceinline__ void evict_select(EvictShared& sh, const EvictArgs& a
         const int y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
       }
-      if (lane == 31) sh.warp_sum[warp][0] = incl;
+      if (lane == 31) sh.warp_sum[warp] = incl;
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < kEvictWarps; ++i) incl += i < warp ? sh.warp_sum[i][0] : 0;
+      for (int i = 0; i < kEvictWarps; ++i) incl += i < warp ? sh.warp_sum[i] : 0;
       if (incl - sum < need && incl >= need) {
         sh.prefix = (prefix << 8) | static_cast<uint32_t>(digit);
         sh.need = need - (incl - sum);
