@@ -174,7 +174,8 @@ PA_API size_t pa_paged_attention_accumulate_workspace_size(int num_seqs, int num
  *                 and both calls may share it in stream order.
  * Everything else is as in pa_paged_attention. Weights are formed in fp32 from the unrounded scores. A block
  * id outside the pool (PA_DEVERR_BLOCK_ID) makes its sequence's scores NaN up to its length in the kv heads
- * that read it; an invalid length (PA_DEVERR_CONTEXT_LEN) leaves the sequence's scores as they are.
+ * that read it; an invalid length (PA_DEVERR_CONTEXT_LEN), any past max_context_len among them, leaves the
+ * sequence's scores as they are.
  */
 PA_API pa_status pa_paged_attention_accumulate(void* out, float* scores, int score_stride, const void* query,
                                                pa_dtype q_dtype, const void* key_cache, const void* value_cache,

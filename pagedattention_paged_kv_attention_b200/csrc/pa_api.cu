@@ -222,6 +222,7 @@ pa_status build_launch(AttnLaunch* l, const AttnPlan& plan, void* out, const voi
   a.partition_size = ps;
   a.num_partitions = partitions;
   a.num_items = static_cast<unsigned int>(items);
+  a.max_tokens = static_cast<int>(std::min<long long>(static_cast<long long>(partitions) * ps, 0x7fffffffLL));
   a.scale_log2 = scale * pa::kLog2e;
   a.scale_block_stride = scale_block_stride(kv_dtype, num_kv_heads);
 #ifdef PA_TRACE
@@ -313,6 +314,7 @@ pa_status decode_rows(void* out, const void* query, pa_dtype q_dtype, const void
                                        block_tables, max_blocks_per_seq, context_lens, num_seqs, num_heads,
                                        num_kv_heads, head_size, block_size, num_blocks, scale, workspace);
   if (built != PA_OK) return built;
+  l.a.max_tokens = max_context_len;
   l.a.q_start = q_start;
   l.a.num_q_tokens = num_q_tokens;
   const bool fp8 = is_fp8(kv_dtype);
@@ -430,6 +432,7 @@ pa_status pa_paged_attention_accumulate(void* out, float* scores, int score_stri
                                        num_kv_heads, head_size, block_size, num_blocks, scale, workspace);
   if (built != PA_OK) return built;
   uint8_t* wsb = static_cast<uint8_t*>(workspace);
+  l.a.max_tokens = max_context_len;  // rows of scores end there, inside the last partition
   l.a.stats = reinterpret_cast<float2*>(wsb + w.stats);
   l.a.logits = reinterpret_cast<float*>(wsb + w.logits);
   l.a.logit_stride = static_cast<long long>(w.stride);

@@ -105,6 +105,7 @@ struct AttnArgs {
   int partition_size;           // tokens per partition, multiple of kPartitionQuantum
   int num_partitions;
   unsigned int num_items;       // num_partitions * num_seqs * head_blocks * subgroups
+  int max_tokens;               // longest context: what the partitions cover, or the caller's max_context_len
   float scale_log2;             // softmax scale * log2(e)
   int scale_block_stride;       // FP8 scales: 0 = per kv head, num_kv_heads = per (block, kv head)
   // Weight accumulation (W instantiations only): the scaled scores z = log2(e) * scale * q.k of every
@@ -300,7 +301,7 @@ __device__ __forceinline__ ItemCoord decode_item(unsigned int idx, const AttnArg
 }
 
 __device__ __forceinline__ bool context_len_invalid(int L, const AttnArgs& a) {
-  return L < 0 || L > a.max_blocks_per_seq * a.block_size || L > a.num_partitions * a.partition_size;
+  return L < 0 || L > a.max_blocks_per_seq * a.block_size || L > a.max_tokens;
 }
 
 // How a sequence enters the work order: its full partitions, whether it has one more item (a partial
