@@ -374,7 +374,8 @@ PA_API pa_status pa_reshape_and_cache(const void* key, const void* value, pa_dty
  *  key_cache, value_cache, k_scale, v_scale, slot_mapping   as in pa_reshape_and_cache (slots are distinct).
  *  positions      [num_axes][num_tokens] int32 (negative positions turn backwards).
  *  inv_freq       [rotary_size / 2] fp32, the angle per position of each pair.
- *  freq_axis      [rotary_size / 2] int32; a pair whose axis is outside [0, num_axes) is not turned.
+ *  freq_axis      [rotary_size / 2] int32; a pair whose axis is outside [0, num_axes) is turned by the angle 0,
+ *                 and its inv_freq is not used.
  * Supported: head_size a multiple of 8 up to 8192, rotary_size a multiple of 16 up to min(head_size, 512); cache dtype
  * in_dtype, PA_FP8_E4M3 or PA_FP8_E4M3_BLOCK. num_tokens == 0 is a no-op (pointers may then be null).
  */

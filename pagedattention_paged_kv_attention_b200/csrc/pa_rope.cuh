@@ -135,9 +135,11 @@ rope_reshape_and_cache_kernel(const RopeArgs a) {
   const int64_t slot = a.slot_mapping[token];
   for (int i = threadIdx.x; i < half; i += blockDim.x) {
     const int axis = a.freq_axis[i];
-    // An axis outside the table has no position: its pairs stay as they are.
-    const int pos = axis >= 0 && axis < a.num_axes ? a.positions[static_cast<int64_t>(axis) * a.num_tokens + token] : 0;
-    const double turns = static_cast<double>(pos) * (static_cast<double>(a.inv_freq[i]) * 0.15915494309189535);
+    // An axis outside the table has no position: its pairs are turned by 0, whatever their frequency holds.
+    const bool known = axis >= 0 && axis < a.num_axes;
+    const int pos = known ? a.positions[static_cast<int64_t>(axis) * a.num_tokens + token] : 0;
+    const float freq = known ? a.inv_freq[i] : 0.f;
+    const double turns = static_cast<double>(pos) * (static_cast<double>(freq) * 0.15915494309189535);
     sincospif(2.0f * static_cast<float>(turns - rint(turns)), &sn[i], &cs[i]);
   }
   __syncthreads();
