@@ -154,7 +154,9 @@ PA_API pa_status pa_paged_attention(void* out, const void* query, pa_dtype q_dty
  * Workspace bytes of pa_paged_attention_accumulate: pa_paged_attention_workspace_size(...) at its partition
  * size, plus the scaled scores of the step, 4 * num_seqs * num_heads * round_up(max_context_len, 64) bytes,
  * and softmax statistics of 8 bytes per (sequence, head, partition). Returns 0 if the arguments are invalid.
- * Makes no CUDA call.
+ * Makes no CUDA call. The size is that of these arguments and no bound for smaller ones: a smaller batch, or a
+ * shorter max_context_len, is cut into more partitions and may need more. A buffer for calls of several sizes
+ * takes the largest of what the query gives for each.
  */
 PA_API size_t pa_paged_attention_accumulate_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
                                                            int head_size, int max_context_len, int partition_size);
@@ -296,6 +298,9 @@ PA_API pa_status pa_paged_prefill_accumulate(void* out, float* scores, int score
 /*
  * Workspace bytes of pa_paged_cross_attention: the header, and fp32 partial results when the keys are split
  * over several CTAs (few query rows over long contexts). 0 if the arguments are invalid. Makes no CUDA call.
+ * The size is that of these arguments and no bound for smaller ones: 32 prompts of 512 rows may need the header
+ * alone, and one of them, or the decode steps after it (max_q_len 1), split keys and need megabytes. A buffer for
+ * calls of several sizes takes the largest of what the query gives for each.
  */
 PA_API size_t pa_paged_cross_attention_workspace_size(int num_seqs, int num_q_tokens, int num_heads,
                                                       int num_kv_heads, int head_size, int max_q_len,

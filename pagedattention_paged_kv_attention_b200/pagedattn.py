@@ -338,7 +338,9 @@ def accumulate_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_
 
 def make_accumulate_workspace(num_seqs, num_heads, num_kv_heads, head_size, max_context_len, partition_size=0,
                               device="cuda") -> torch.Tensor:
-    """A zeroed workspace for paged_attention_accumulate (paged_attention of these sizes may share it)."""
+    """A zeroed workspace for paged_attention_accumulate of these sizes (paged_attention of these sizes may share it).
+    Smaller batches or contexts may need more; a buffer for several sizes takes the largest of their
+    accumulate_workspace_size."""
     n = accumulate_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_context_len, partition_size)
     if n == 0:
         raise ValueError("invalid sizes for a workspace")
@@ -411,7 +413,8 @@ def paged_prefill_accumulate(out, scores, query, key_cache, value_cache, block_t
 
 def make_cross_workspace(num_seqs, num_q_tokens, num_heads, num_kv_heads, head_size, max_q_len, max_context_len,
                          device="cuda") -> torch.Tensor:
-    """A zeroed workspace for paged_cross_attention of these sizes."""
+    """A zeroed workspace for paged_cross_attention of these sizes. Fewer sequences or rows (decode steps, max_q_len 1)
+    split their keys and may need more; a buffer for several sizes is the largest of theirs."""
     n = lib.pa_paged_cross_attention_workspace_size(num_seqs, num_q_tokens, num_heads, num_kv_heads, head_size,
                                                     max_q_len, max_context_len)
     if n == 0:
