@@ -548,7 +548,9 @@ def evict_tokens(kept, new_lens, scores_out, scores, key_cache, value_cache, blo
     """Cut every sequence to at most `budget` tokens: per kv head the first num_sink, the last num_recent
     and the highest scores[S,Hkv,stride] between them stay, moved together in order into the blocks of
     dst_block_tables (block_tables itself: in place). Writes kept[S,Hkv,budget], new_lens[S] and
-    scores_out. Per-block FP8 scales (a 2-D k_scale) are refused: their codes cannot change blocks."""
+    scores_out. k_scale says which scales an FP8 cache has; a cache given without it is taken to have per-head
+    ones, whose codes move as they are. Per-block scales (a 2-D k_scale) are refused: their codes cannot change
+    blocks, so a cache that has them must be given with its k_scale."""
     i32 = torch.int32
     try:
         dev, ks, ss = scores.get_device(), key_cache.shape, scores.shape
@@ -574,6 +576,10 @@ def evict_tokens(kept, new_lens, scores_out, scores, key_cache, value_cache, blo
                 value_cache=(value_cache, None, 4), block_tables=(block_tables, i32, 2),
                 dst_block_tables=(dst_block_tables, i32, 2), context_lens=(context_lens, i32, 1),
                 workspace=(workspace, None, workspace.dim() if isinstance(workspace, torch.Tensor) else 1))
+    if k_scale is not None:
+        _arg(k_scale, "k_scale", _F32, (1, 2))
+        _scales(k_scale, "k_scale", key_cache)
+        _device(k_scale, "k_scale")
     st = lib.pa_evict_tokens(
         kept.data_ptr(), new_lens.data_ptr(), scores_out.data_ptr(), scores.data_ptr(), ss[2], key_cache.data_ptr(),
         value_cache.data_ptr(), cache_code(key_cache, k_scale), block_tables.data_ptr(), block_tables.shape[1],
