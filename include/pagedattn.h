@@ -281,9 +281,13 @@ PA_API size_t pa_paged_prefill_accumulate_workspace_size(int num_q_tokens, int n
  *  score_stride   entries between the rows, >= max_context_len.
  *  max_context_len  >= every context_lens[s]; sizes the grid.
  *  workspace      >= pa_paged_prefill_accumulate_workspace_size(...) bytes, its header zeroed once.
- * Everything else is as in pa_paged_prefill. Weights are formed in fp32 from the unrounded scores. A chunk
- * outside its context, a chunk that max_q_len's grid does not cover, or a length past max_context_len
- * (PA_DEVERR_CONTEXT_LEN) leaves the sequence's scores as they are; tokens seen by a counted row that also sees a block outside the pool (PA_DEVERR_BLOCK_ID) get NaN.
+ * Everything else is as in pa_paged_prefill. Weights are formed in fp32 from unrounded scores and each row's
+ * softmax statistics. With per-block scales (PA_FP8_E4M3_BLOCK) the statistics are those of out, whose keys are
+ * code * scale in f16, while a weight's own score takes the scale in fp32: a row's weights then add up to one
+ * within what f16's rounding of the keys does to its scores. A chunk outside its context, a chunk that
+ * max_q_len's grid does not cover, or a length past max_context_len (PA_DEVERR_CONTEXT_LEN) leaves the sequence's
+ * scores as they are; tokens seen by a counted row that also sees a block outside the pool (PA_DEVERR_BLOCK_ID)
+ * get NaN.
  */
 PA_API pa_status pa_paged_prefill_accumulate(void* out, float* scores, int score_stride, const void* query,
                                              pa_dtype q_dtype, const void* key_cache, const void* value_cache,
@@ -452,7 +456,8 @@ PA_API pa_status pa_copy_blocks_layers(void* const* key_caches, void* const* val
  *                 (pa_bm_plan_evict gives both tables). The first ceil(min(L, budget) / block_size) entries
  *                 are read. Entry i may be the sequence's own block_tables entry i (compaction in place;
  *                 block_tables may be passed itself) if no other sequence reads that block; any other
- *                 destination must be a block that no sequence of the call reads. Destinations of one call are distinct.
+ *                 destination must be a block that no sequence of the call reads. Destinations of one call are
+ *                 distinct.
  *  budget >= 1, num_sink >= 0, num_recent >= 0, num_sink + num_recent <= budget;
  *  max_dst_blocks_per_seq * block_size >= min(budget, max_context_len).
  *  workspace      >= PA_WORKSPACE_HEADER_BYTES, zeroed once; its first word is the device error word.

@@ -28,7 +28,6 @@ namespace {
 // long (fewer, larger items mean fewer split-K partials to write and merge; the order keeps the tail
 // short), and never more than 32 partitions (the merge's cost grows with them): 768 for the 70B-shape
 // batch, 512-768 for 7B, 1024 for 8 x 32768 tokens.
-constexpr int kPlanSMs = 148;            // B200 SM count; planning is a pure function of the sizes
 constexpr int kPlanItemsPerCta = 5;
 constexpr int kPlanMaxPartitions = 32;
 constexpr int kMinAutoPartition = 256;
@@ -39,6 +38,7 @@ using pa_host::elem_bytes;
 using pa_host::is_16bit;
 using pa_host::is_dtype;
 using pa_host::is_fp8;
+using pa_host::kPlanSMs;
 using pa_host::scale_block_stride;
 using pa_host::round_up;
 using pa_host::tensor_map_encoder;

@@ -434,7 +434,7 @@ __device__ __forceinline__ ItemCoord decode_ordered(unsigned int t, const AttnAr
 // BS: FP8 cache with per-(block, kv head) scales (args.scale_block_stride != 0); a separate
 // instantiation so that the per-head FP8 path carries none of its work.
 // kDecodeWeights (W): also writes every token's scaled score and each item's softmax statistics, from which
-// attention_weights_kernel (pa_weights.cuh) forms the normalised weights. Kept apart from the plain
+// attention_finish_kernel (pa_weights.cuh) forms the normalised weights. Kept apart from the plain
 // instantiations, whose code and results it leaves as they are. The sum of a W item's statistics takes
 // the weights before their rounding to 16 bits (l_run takes the rounded ones that enter P V): scores
 // accumulate over thousands of steps and carry fp32 accuracy.

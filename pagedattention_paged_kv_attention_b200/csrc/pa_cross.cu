@@ -19,7 +19,7 @@ CrossPlan plan_cross(int num_seqs, int num_q_tokens, int num_heads, int num_kv_h
   const long long ctas = static_cast<long long>(pa_host::ceil_div(max_q_len, tile_tokens * pa::pf::kTiles)) *
                          num_kv_heads * num_seqs;
   const int tiles = std::max(1, pa_host::ceil_div(max_context_len, pa::pf::kKvTile));
-  const long long want = ctas > 0 ? (2 * 148 + ctas - 1) / ctas : 1;
+  const long long want = ctas > 0 ? (2 * pa_host::kPlanSMs + ctas - 1) / ctas : 1;
   const int splits = static_cast<int>(std::max<long long>(1, std::min<long long>(want, tiles / 4)));
   p.split_tiles = pa_host::ceil_div(tiles, splits);
   p.splits = pa_host::ceil_div(tiles, p.split_tiles);

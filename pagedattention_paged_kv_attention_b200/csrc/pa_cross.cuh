@@ -44,7 +44,8 @@ cross_merge_kernel(const PrefillArgs a) {
   const float inv = 1.f / wsum;
   T* dst = static_cast<T*>(a.out) + rowi * D + lane * kPer;
 #pragma unroll
-  for (int k = 0; k < kPer; k += 2) *reinterpret_cast<uint32_t*>(dst + k) = pack_pair<T>(acc[k] * inv, acc[k + 1] * inv);
+  for (int k = 0; k < kPer; k += 2)
+    *reinterpret_cast<uint32_t*>(dst + k) = pack_pair<T>(acc[k] * inv, acc[k + 1] * inv);
 }
 
 }  // namespace pf

@@ -400,7 +400,8 @@ evict_kernel(const EvictArgs a) {
     auto column = [&](int strip) {  // this lane's column of the strip; null when it has none
       const bool value = strip >= strips;
       const int col = ((value ? strip - strips : strip) << (a.log_lanes + 4)) + lane_col;
-      return col < a.row_bytes ? (value ? a.value_cache : a.key_cache) + static_cast<size_t>(h) * a.row_bytes + col : nullptr;
+      if (col >= a.row_bytes) return static_cast<uint8_t*>(nullptr);
+      return (value ? a.value_cache : a.key_cache) + static_cast<size_t>(h) * a.row_bytes + col;
     };
     auto next = [&](Cursor& c) {
       if (++c.strip == 2 * strips) {

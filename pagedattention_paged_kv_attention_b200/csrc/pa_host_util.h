@@ -14,6 +14,8 @@
 
 namespace pa_host {
 
+constexpr int kPlanSMs = 148;  // B200 SM count; planning is a pure function of the sizes
+
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // ceil(a / b) for a >= 0, b > 0, without forming a + b - 1 (which overflows near INT_MAX).

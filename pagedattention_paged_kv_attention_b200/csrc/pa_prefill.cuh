@@ -192,8 +192,9 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr bool kIsCross = MODE == kCross;
   const int split = kIsCross ? static_cast<int>(blockIdx.x) % a.splits : 0;
+  // Longest prefixes first.
   const int pair =
-      a.num_pairs - 1 - (kIsCross ? static_cast<int>(blockIdx.x) / a.splits : static_cast<int>(blockIdx.x));  // longest prefixes first
+      a.num_pairs - 1 - (kIsCross ? static_cast<int>(blockIdx.x) / a.splits : static_cast<int>(blockIdx.x));
   const int kvh = blockIdx.y, s = blockIdx.z;
   const int G = a.group;
 

@@ -40,7 +40,8 @@ struct RopeArgs {
   int64_t query_out_stride, query_stride, key_stride, value_stride;  // elements between tokens
   int num_tokens, num_axes, num_heads, num_kv_heads, head_size, rotary, block_size, num_blocks, scale_stride,
       units;                          // of a head: those of rotated pairs, and plain vectors
-  unsigned inv_units, inv_plain;      // ceil(2^32 / units) (0: one unit), ceil(2^32 / (head_size / 8)): a quotient is a product's high word
+  // ceil(2^32 / units) (0: one unit) and ceil(2^32 / (head_size / 8)): a quotient is a product's high word.
+  unsigned inv_units, inv_plain;
 };
 
 // E4M3 codes of x / scale, as __fdiv_rn and a conversion give them. The product with 1 / scale is within 2 units

@@ -1,5 +1,5 @@
-"""The workspaces of scoring decode and cross attention without a GPU: a size holds for the arguments it was asked for. A
-smaller call may need more, its own query says how much, and a buffer below that is refused before any CUDA call."""
+"""The workspaces of scoring decode and cross attention without a GPU: a size holds for the arguments it was asked for.
+A smaller call may need more, its own query says how much, and a buffer below that is refused before any CUDA call."""
 import pytest
 
 import test_abi_operators as A

@@ -1,4 +1,4 @@
-"""The scales that evict_tokens is given: per-head ones of the cache are accepted, others refused before anything runs."""
+"""The scales that evict_tokens is given: per-head ones of the cache are accepted, others refused before it runs."""
 import pytest
 import torch
 
@@ -16,8 +16,8 @@ def P():
 def call(P, st, k_scale):
     kept = torch.full((2, 2, 30), -99, dtype=torch.int32, device="cuda")
     new = torch.full((2,), -99, dtype=torch.int32, device="cuda")
-    P.evict_tokens(kept, new, st["scores"], st["scores"], st["kc"], st["vc"], st["table"], st["table"], st["cl"], 30, 2, 5,
-                   st["max_len"], P.make_evict_workspace(), k_scale=k_scale)
+    P.evict_tokens(kept, new, st["scores"], st["scores"], st["kc"], st["vc"], st["table"], st["table"], st["cl"], 30, 2,
+                   5, st["max_len"], P.make_evict_workspace(), k_scale=k_scale)
     return kept, new
 
 

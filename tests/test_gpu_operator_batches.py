@@ -1,6 +1,6 @@
-"""Calls with more work items than the GPU has SMs, so that CTAs take several items one after another: scoring decode and
-single-token cross attention (tickets, in order of size or, for large batches, as they come), scoring prefill (items
-dealt and drawn, several rings of them a CTA) and eviction (more tokens a CTA than its registers hold)."""
+"""Calls with more work items than the GPU has SMs, so that CTAs take several items one after another: scoring decode
+and single-token cross attention (tickets, in order of size or, for large batches, as they come), scoring prefill
+(items dealt and drawn, several rings of them a CTA) and eviction (more tokens a CTA than its registers hold)."""
 import pytest
 import torch
 
