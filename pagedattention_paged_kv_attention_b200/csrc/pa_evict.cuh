@@ -392,7 +392,7 @@ evict_kernel(const EvictArgs a) {
     }
     evict_sync(wo == w ? ctas : 1);  // in place, every CTA has read the stage's scores, which are now written over
     // Step = (round, strip); loads and stores have a cursor each, and go two steps at a time (keys and values are an
-    // even number). A later round's rows come from slots above this round's.
+    // even number). The rows of later rounds come from slots above.
     struct Cursor {
       int round, strip;
       const uint32_t* from;
